@@ -36,7 +36,8 @@
  *     device current at spmv_create_csr and must be used with it current.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream). Work is enqueued on it asynchronously unless stated.
- *   - Index type is int32 (signed; negatives are rejected), values are fp32.
+ *   - Index type is int32 (signed; negatives are rejected), values are fp32
+ *     (the operators on dense tables at the end name their own types).
  *   - Ownership: the caller owns the CSR arrays, x and y. The handle BORROWS
  *     the CSR arrays (it reads them again in spmv_run(SPMV_CSR) and the
  *     COO format reuses colIdx/value), so they must stay alive and unchanged
@@ -346,6 +347,115 @@ int spmv_destroy(spmv_handle h);
 int spmv_run_csr_noalloc(int32_t numRows, int32_t numCols, int32_t nnz,
                          const int32_t *d_rowPtrs, const int32_t *d_colIdx,
                          const float *d_value, const float *d_x, float *d_y, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Dense tables of a language model: 4-bit matrices and token lookups
+ *
+ * The matrix-vector product at the end of a decoding step is as bound by the
+ * bytes of its matrix as the sparse ones above; its storage format is four
+ * bits per entry with a scale for each group of a row's columns. The lookup
+ * that such a step begins with is the product of a matrix with one entry per
+ * row (at the token's column) and a dense table, and its gradient is the
+ * transposed product, summed by token. One 4-bit table can serve both ends.
+ *
+ * These calls take the caller's arrays as they are: no handle, nothing kept
+ * from one call for the next, nothing allocated, never a synchronisation, so
+ * every one of them can be captured into a CUDA graph (after one call outside
+ * capture on the device). They run on the current device; every pointer is a
+ * device pointer of that device, aligned to its element's size. Leading
+ * dimensions (ld...) count elements (codes: bytes) from one row to the next
+ * and are at least the row's width; 64-bit offsets throughout. Sums and
+ * scales are computed in fp32 and results rounded once to the output's type.
+ * Results are the same from call to call: no sum depends on the order in
+ * which blocks run.
+ * ------------------------------------------------------------------------- */
+typedef enum { SPMV_F32 = 0, SPMV_F16 = 1, SPMV_BF16 = 2 } spmv_dtype;
+
+/* A rows x cols matrix held in 4 bits:
+ *   A[r][k] = scale[r][k / group] * (code[r][k] - zero[r][k / group]),
+ * code in 0..15, two to a byte: column k of row r is the low half (k even) or
+ * the high half (k odd) of codes[r * ld_codes + k / 2]; the unused half byte
+ * of an odd row end is ignored. group is 32, 64 or 128 (the last group of a
+ * row may be partial); zeros == NULL means 8 everywhere. A view: the caller
+ * owns the arrays. */
+typedef struct {
+  int32_t rows, cols, group;
+  int32_t scale_type;      /* spmv_dtype of scales */
+  uint8_t *codes;
+  int64_t ld_codes;        /* bytes, >= ceil(cols / 2) */
+  void *scales;            /* one per row and group */
+  int64_t ld_scales;       /* elements, >= ceil(cols / group) */
+  uint8_t *zeros;          /* one byte (0..15) per row and group, or NULL */
+  int64_t ld_zeros;        /* bytes, >= ceil(cols / group) */
+} spmv_q4;
+
+/* Convert a dense matrix W (rows x cols of wType, leading dimension ldw) into
+ * a->codes, a->scales and, if not NULL, a->zeros. Per group of a row, with the
+ * quotient and the rounding (to nearest, ties to even) in fp32:
+ *   without zeros: scale = max|w| / 7, zero = 8;
+ *   with zeros:    scale = (max(w, 0) - min(w, 0)) / 15,
+ *                  zero = clamp(round(-min(w, 0) / scale), 0, 15);
+ *   scale rounded to scale_type, then code = clamp(round(w / scale) + zero, 0, 15).
+ * A scale that rounds to 0 gives codes equal to zero (values 0; zero = 0 where
+ * zeros are kept). A group with an infinity or a NaN, or whose scale overflows
+ * scale_type, gets a scale that is not finite and codes equal to zero, so that
+ * all its values are NaN: a fault in the weights shows in every product.
+ *   d_back: NULL, or rows x cols of wType (leading dimension ld_back) that
+ *   receives the values A[r][k] the codes stand for; it may be d_w itself
+ *   (with ld_back == ldw). An odd row end's unused half byte is written 0.
+ * Asynchronous; one kernel. */
+int spmv_q4_quantize(const spmv_q4 *a, spmv_dtype wType, const void *d_w, int64_t ldw,
+                     void *d_back, int64_t ld_back, void *stream);
+
+/* y_j <- A x_j + c_j for n vectors (n >= 0): x_j = d_x + j * ldx (cols of
+ * xType), y_j = d_y + j * ldy and c_j = d_c + j * ldc (rows of yType).
+ *   d_c: NULL for none; it may be d_y itself (with ldc == ldy: the library's
+ *   multiply-and-accumulate). Otherwise y may not overlap x or c
+ *   (SPMV_ERR_INVALID_ARG). xType and yType are independent.
+ * Products are exact and summed in fp32, a group's sum times its scale, so
+ * sum over a group of |code - zero| |x| has to stay within fp32. Per entry the
+ * result is within (ceil(cols / 16) + 32) * 2^-22 * (sum_k |A[r][k] x[k]| +
+ * |c|) of the exact value before the rounding to yType. Asynchronous. The
+ * matrix is read once for every 16 vectors (8 of fp32). */
+int spmv_q4_run(const spmv_q4 *a, int32_t n, spmv_dtype xType, const void *d_x, int64_t ldx,
+                const void *d_c, int64_t ldc, spmv_dtype yType, void *d_y, int64_t ldy,
+                void *stream);
+
+/* out[t][:] <- scale * table[token[t]][:] for nTokens tokens: table is vocab x
+ * dim of tableType, out is nTokens x dim of outType. Tokens are int32
+ * (indexBytes 4) or int64 (8). A token outside 0 .. vocab-1 (a padding token of
+ * -1, say) gives a row of zeros and reads nothing. out may not overlap table.
+ * Asynchronous; one kernel. */
+int spmv_embed(int32_t vocab, int32_t dim, spmv_dtype tableType, const void *d_table,
+               int64_t ld_table, int32_t nTokens, int32_t indexBytes, const void *d_tokens,
+               float scale, spmv_dtype outType, void *d_out, int64_t ld_out, void *stream);
+
+/* As spmv_embed from a 4-bit table: out[t][k] <- scale * A[token[t]][k], with
+ * vocab = a->rows and dim = a->cols; the product with scale is rounded in fp32.
+ * d_tokens == NULL stands for 0, 1, ..., nTokens - 1 (with nTokens = a->rows
+ * and scale 1: the whole matrix back in dense form). Asynchronous; one kernel. */
+int spmv_embed_q4(const spmv_q4 *a, int32_t nTokens, int32_t indexBytes, const void *d_tokens,
+                  float scale, spmv_dtype outType, void *d_out, int64_t ld_out, void *stream);
+
+/* Gradient of spmv_embed with respect to its table: with g (nTokens x dim of
+ * gType) the gradient of out,
+ *   dtable[v][:] <- scale * sum over t with token[t] = v of g[t][:]   (accumulate = 0)
+ *   dtable[v][:] <- dtable[v][:] + the same                           (accumulate = 1)
+ * for every row v of vocab. accumulate = 0 writes the whole of dtable (zeros
+ * where no token falls), accumulate = 1 only the rows with a token. Tokens are
+ * sorted, equal ones in order, and each row's terms are summed in fp32 in that
+ * order, a fixed number at a time; tokens outside 0 .. vocab-1 add nothing.
+ *   d_work: scratch of at least spmv_embed_grad_workspace(...) bytes, 16-byte
+ *   aligned, free again when the call's work on `stream` is done
+ *   (SPMV_ERR_INVALID_ARG when smaller; may be NULL when that is 0).
+ * g, dtable and d_work may not overlap. Asynchronous. */
+int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void *d_g, int64_t ld_g,
+                    int32_t nTokens, int32_t indexBytes, const void *d_tokens, float scale,
+                    int32_t accumulate, spmv_dtype tableType, void *d_dtable, int64_t ld_dtable,
+                    void *d_work, int64_t workBytes, void *stream);
+
+/* Scratch bytes that spmv_embed_grad needs, into *bytes. Host-only. */
+int spmv_embed_grad_workspace(int32_t vocab, int32_t dim, int32_t nTokens, int64_t *bytes);
 
 /* Static English text for a status code. */
 const char *spmv_status_string(int status);

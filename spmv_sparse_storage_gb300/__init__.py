@@ -29,6 +29,10 @@ FORMATS = {"COO": SPMV_COO, "CSR": SPMV_CSR, "ELL": SPMV_ELL, "HYB": SPMV_HYB,
            "JDS": SPMV_JDS, "AUTO": SPMV_AUTO, "SELL": SPMV_SELL, "XBLOCK": SPMV_XBLOCK}
 FORMAT_NAMES = {v: k for k, v in FORMATS.items()}
 
+# element types of the dense-table operators (spmv_dtype)
+SPMV_F32, SPMV_F16, SPMV_BF16 = range(3)
+DTYPES = {torch.float32: SPMV_F32, torch.float16: SPMV_F16, torch.bfloat16: SPMV_BF16}
+
 SPMV_OK = 0
 SPMV_ERR_INVALID_ARG = -1
 SPMV_ERR_BAD_ROWPTRS = -2
@@ -62,6 +66,13 @@ class spmv_arrays(C.Structure):
                 ("coo_value_f64", C.c_void_p)]
 
 
+class spmv_q4(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("cols", C.c_int32), ("group", C.c_int32),
+                ("scale_type", C.c_int32), ("codes", C.c_void_p), ("ld_codes", C.c_int64),
+                ("scales", C.c_void_p), ("ld_scales", C.c_int64), ("zeros", C.c_void_p),
+                ("ld_zeros", C.c_int64)]
+
+
 class spmv_cg_info(C.Structure):
     _fields_ = [("iterations", C.c_int32), ("status", C.c_int32),
                 ("residual_norm", C.c_double), ("y_norm", C.c_double)]
@@ -90,6 +101,19 @@ _SIGS = {
     "spmv_export": (C.c_int, [_H, C.c_int, C.POINTER(spmv_arrays)]),
     "spmv_destroy": (C.c_int, [_H]),
     "spmv_run_csr_noalloc": (C.c_int, [C.c_int32, C.c_int32, C.c_int32, _P, _P, _P, _P, _P, _P]),
+    "spmv_q4_quantize": (C.c_int, [C.POINTER(spmv_q4), C.c_int, _P, C.c_int64, _P, C.c_int64,
+                                   _P]),
+    "spmv_q4_run": (C.c_int, [C.POINTER(spmv_q4), C.c_int32, C.c_int, _P, C.c_int64, _P,
+                              C.c_int64, C.c_int, _P, C.c_int64, _P]),
+    "spmv_embed": (C.c_int, [C.c_int32, C.c_int32, C.c_int, _P, C.c_int64, C.c_int32, C.c_int32,
+                             _P, C.c_float, C.c_int, _P, C.c_int64, _P]),
+    "spmv_embed_q4": (C.c_int, [C.POINTER(spmv_q4), C.c_int32, C.c_int32, _P, C.c_float, C.c_int,
+                                _P, C.c_int64, _P]),
+    "spmv_embed_grad": (C.c_int, [C.c_int32, C.c_int32, C.c_int, _P, C.c_int64, C.c_int32,
+                                  C.c_int32, _P, C.c_float, C.c_int32, C.c_int, _P, C.c_int64,
+                                  _P, C.c_int64, _P]),
+    "spmv_embed_grad_workspace": (C.c_int, [C.c_int32, C.c_int32, C.c_int32,
+                                            C.POINTER(C.c_int64)]),
     "spmv_status_string": (C.c_char_p, [C.c_int]),
     "spmv_last_cuda_error": (C.c_int, []),
     "spmv_launch_count": (C.c_uint64, []),
@@ -253,6 +277,165 @@ def spmv_run_csr_noalloc(num_rows, num_cols, nnz, row_ptrs, col_idx, value, x, y
            "spmv_run_csr_noalloc")
 
 
+# --- dense tables: 4-bit matrices and token lookups --------------------------------
+def _dtype(t, what):
+    try:
+        return DTYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"{what}: expected float32, float16 or bfloat16, got {t.dtype}") from None
+
+
+def _matrix(t, what, dtype=None):
+    """(pointer, rows, columns, leading dimension) of a CUDA tensor of one or
+    two dimensions whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) == 1:
+        rows, cols = 1, shape[0]
+        ld = cols
+        inner = t.stride(0)
+    elif len(shape) == 2:
+        rows, cols = shape
+        outer, inner = t.stride()
+        ld = outer if rows > 1 else cols
+    else:
+        raise ValueError(f"{what}: expected one or two dimensions, got {len(shape)}")
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{what}: expected contiguous rows")
+    return t.data_ptr() or None, rows, cols, ld
+
+
+def _tokens(t):
+    """(pointer, count, bytes each) of a contiguous CUDA tensor of tokens."""
+    if t.dtype == torch.int64:
+        size = 8
+    elif t.dtype == torch.int32:
+        size = 4
+    else:
+        raise TypeError(f"tokens: expected int32 or int64, got {t.dtype}")
+    return _ptr(t), t.numel(), size
+
+
+def _q4_view(codes, scales, group, cols, zeros):
+    """The spmv_q4 of the arrays (which the caller keeps alive)."""
+    cp, rows, width, ldc = _matrix(codes, "codes", torch.uint8)
+    sp_, srows, swidth, lds = _matrix(scales, "scales")
+    groups = -(-cols // group) if group in (32, 64, 128) else 0  # else the library refuses
+    if srows != rows or swidth < groups or width < (cols + 1) // 2:
+        raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not "
+                         f"hold {cols} columns in groups of {group}")
+    zp, ldz = None, 0
+    if zeros is not None:
+        zp, zrows, zwidth, ldz = _matrix(zeros, "zeros", torch.uint8)
+        if zrows != rows or zwidth < groups:
+            raise ValueError(f"zeros {tuple(zeros.shape)} do not match scales "
+                             f"{tuple(scales.shape)}")
+    return spmv_q4(rows, cols, group, _dtype(scales, "scales"), cp, ldc, sp_, lds, zp, ldz)
+
+
+def spmv_q4_quantize(w, codes, scales, group, zeros=None, back=None, stream=None):
+    """Convert ``w`` [rows, cols] into 4-bit ``codes`` [rows, ceil(cols/2)]
+    (uint8), ``scales`` [rows, ceil(cols/group)] and, if given, ``zeros``
+    (uint8). ``back`` (shape and type of ``w``; may be ``w``) receives the
+    values that the codes stand for."""
+    wp, rows, cols, ldw = _matrix(w, "w")
+    a = _q4_view(codes, scales, group, cols, zeros)
+    if a.rows != rows:
+        raise ValueError(f"w has {rows} rows, codes {a.rows}")
+    bp, ldb = None, 0
+    if back is not None:
+        bp, brows, bcols, ldb = _matrix(back, "back", w.dtype)
+        if (brows, bcols) != (rows, cols):
+            raise ValueError("back: expected the shape of w")
+    _check(_lib.spmv_q4_quantize(C.byref(a), _dtype(w, "w"), wp, ldw, bp, ldb, _stream(stream)),
+           "spmv_q4_quantize")
+
+
+def spmv_q4_run(codes, scales, group, x, y, c=None, zeros=None, stream=None):
+    """y <- A x + c for a 4-bit A [rows, cols]: ``x`` [cols] or [n, cols], ``y``
+    and ``c`` (optional; may be ``y``) [rows] or [n, rows]."""
+    xp, n, cols, ldx = _matrix(x, "x")
+    yp, yn, rows, ldy = _matrix(y, "y")
+    a = _q4_view(codes, scales, group, cols, zeros)
+    if yn != n or a.rows != rows:
+        raise ValueError(f"y {tuple(y.shape)} does not fit x {tuple(x.shape)} and {a.rows} rows")
+    cp, ldc = None, 0
+    if c is not None:
+        cp, cn, crows, ldc = _matrix(c, "c", y.dtype)
+        if (cn, crows) != (n, rows):
+            raise ValueError("c: expected the shape of y")
+    _check(_lib.spmv_q4_run(C.byref(a), n, _dtype(x, "x"), xp, ldx, cp, ldc, _dtype(y, "y"), yp,
+                            ldy, _stream(stream)), "spmv_q4_run")
+
+
+def _lookup_out(out, n):
+    op, rows, dim, ldo = _matrix(out, "out")
+    if rows != n:
+        raise ValueError(f"out has {rows} rows for {n} tokens")
+    return op, dim, ldo
+
+
+def spmv_embed(table, tokens, out, scale=1.0, stream=None):
+    """out[t] <- scale * table[tokens[t]] ([vocab, dim] and [n, dim]); a token
+    outside 0 .. vocab-1 gives a row of zeros."""
+    tp, vocab, dim, ldt = _matrix(table, "table")
+    kp, n, size = _tokens(tokens)
+    op, odim, ldo = _lookup_out(out, n)
+    if odim != dim:
+        raise ValueError(f"out has {odim} columns, the table {dim}")
+    _check(_lib.spmv_embed(vocab, dim, _dtype(table, "table"), tp, ldt, n, size, kp, scale,
+                           _dtype(out, "out"), op, ldo, _stream(stream)), "spmv_embed")
+
+
+def spmv_embed_q4(codes, scales, group, tokens, out, scale=1.0, zeros=None, stream=None):
+    """As spmv_embed from a 4-bit table; ``tokens`` None: rows 0 .. len(out)-1."""
+    kp, n, size = _tokens(tokens) if tokens is not None else (None, None, 4)
+    op, dim, ldo = _lookup_out(out, n if n is not None else
+                               (out.shape[0] if out.dim() == 2 else 1))
+    a = _q4_view(codes, scales, group, dim, zeros)
+    if n is None:
+        n = out.shape[0] if out.dim() == 2 else 1
+    _check(_lib.spmv_embed_q4(C.byref(a), n, size, kp, scale, _dtype(out, "out"), op, ldo,
+                              _stream(stream)), "spmv_embed_q4")
+
+
+def spmv_embed_grad_workspace(vocab, dim, n_tokens):
+    """Scratch bytes of spmv_embed_grad."""
+    b = C.c_int64()
+    _check(_lib.spmv_embed_grad_workspace(vocab, dim, n_tokens, C.byref(b)),
+           "spmv_embed_grad_workspace")
+    return b.value
+
+
+def spmv_embed_grad(g, tokens, dtable, scale=1.0, accumulate=False, workspace=None, stream=None):
+    """dtable[v] <- scale * sum of g[t] over the t with tokens[t] = v (added to
+    dtable with ``accumulate``). ``workspace``: a contiguous CUDA tensor of at
+    least spmv_embed_grad_workspace bytes, or None to take one from torch for
+    the call."""
+    gp, n, dim, ldg = _matrix(g, "g")
+    kp, count, size = _tokens(tokens)
+    dp, vocab, ddim, ldd = _matrix(dtable, "dtable")
+    if count != n or ddim != dim:
+        raise ValueError(f"g {tuple(g.shape)}, {count} tokens and dtable "
+                         f"{tuple(dtable.shape)} do not fit")
+    st = _stream(stream)
+    if workspace is None:
+        nbytes = spmv_embed_grad_workspace(vocab, dim, n)
+        # taken on the launching stream, so that torch reuses it only after the call's work
+        if st == torch.cuda.current_stream().cuda_stream:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(st)):
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    _check(_lib.spmv_embed_grad(vocab, dim, _dtype(g, "g"), gp, ldg, n, size, kp, scale,
+                                1 if accumulate else 0, _dtype(dtable, "dtable"), dp, ldd,
+                                _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                st), "spmv_embed_grad")
+
+
 def spmv_status_string(code):
     return _lib.spmv_status_string(code).decode()
 
@@ -408,4 +591,4 @@ class SparseMatrix:
 
 __all__ = [n for n in list(globals()) if n.startswith("spmv_") or n.startswith("SPMV_")] + [
     "SpmvError", "SparseMatrix", "export_tensors", "device_view", "FORMATS", "FORMAT_NAMES",
-    "LIB_PATH"]
+    "LIB_PATH", "DTYPES"]

@@ -129,6 +129,14 @@ void note_launches(int n) { g_launches.fetch_add((unsigned long long)n, std::mem
 
 int record_cuda(cudaError_t e) { return record(e); }
 
+int check_current_device_ptrs(const void* const* ptrs, int n) {
+  int dev = 0;
+  SPMV_TRY(record(cudaGetDevice(&dev)));
+  for (int i = 0; i < n; ++i)
+    if (ptrs[i]) SPMV_TRY(check_device_ptr(ptrs[i], dev));
+  return SPMV_OK;
+}
+
 int num_sms() {
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1265,6 +1273,6 @@ int spmv_set_memory_limit(int64_t bytes) {
   return SPMV_OK;
 }
 
-int spmv_version(void) { return 1 * 10000 + 0 * 100 + 0; }
+int spmv_version(void) { return 1 * 10000 + 1 * 100 + 0; }
 
 }  // extern "C"

@@ -314,6 +314,26 @@ struct ChunkKeyIn {
   }
 };
 
+struct TokenKeyIn {
+  // pass 0: key = token i, or vocab for a token outside 0 .. vocab-1
+  const void* tokens;
+  int wide;  // int64 tokens
+  int vocab;
+  const int* keysIn;
+  const int* valsIn;
+  __device__ void get(long long i, int& key, int& val) const {
+    if (keysIn) {
+      key = keysIn[i];
+      val = valsIn[i];
+    } else {
+      const long long t = wide ? static_cast<const long long*>(tokens)[i]
+                               : (long long)static_cast<const int*>(tokens)[i];
+      key = t >= 0 && t < vocab ? (int)t : vocab;
+      val = (int)i;
+    }
+  }
+};
+
 // Per tile, count keys per digit; hist is digit-major: hist[d * nTiles + tile].
 // All of a thread's keys are loaded before any is counted; equal digits in a
 // warp are counted with one shared atomic (warp match).
@@ -894,6 +914,19 @@ static cudaError_t row_sort(int R, int maxLen, const int* rowPtrs, int* perm, in
                             int** scanScratchOut, cudaStream_t s) {
   return radix_sort(SortIn{rowPtrs, maxLen, nullptr, nullptr}, R, maxLen, perm, scratch,
                     needKeys, sortedKeys, invOut, scanScratchOut, s);
+}
+
+// Scratch: perm[n], then the radix sort's own.
+size_t token_sort_scratch_bytes(int n, int vocab) {
+  return sizeof(int) * (size_t)n + jds_sort_scratch_bytes(n, vocab);
+}
+cudaError_t launch_token_sort(int n, int vocab, const void* tokens, int indexBytes, void* scratch,
+                              const int** posOut, const int** keyOut, cudaStream_t s) {
+  int* perm = static_cast<int*>(scratch);
+  int* unusedScan = nullptr;
+  *posOut = perm;
+  return radix_sort(TokenKeyIn{tokens, indexBytes == 8, vocab, nullptr, nullptr}, n, vocab, perm,
+                    perm + n, true, keyOut, nullptr, &unusedScan, s);
 }
 
 template <class T>

@@ -1,0 +1,68 @@
+// dtypes.cuh -- the element types of the dense-table operators (spmv_dtype)
+// and their conversions from and to fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "internal.h"
+
+namespace spmv {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <class T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) {
+  return __float2half_rn(v);
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// Calls f(T{}) with T = the C++ type of a (checked) spmv_dtype.
+template <class F>
+cudaError_t with_dtype(int type, F&& f) {
+  switch (type) {
+    case SPMV_F16: return f(__half{});
+    case SPMV_BF16: return f(__nv_bfloat16{});
+    default: return f(float{});
+  }
+}
+
+inline bool dtype_ok(int type) { return type >= SPMV_F32 && type <= SPMV_BF16; }
+inline int dtype_bytes(int type) { return type == SPMV_F32 ? 4 : 2; }
+
+// Host-side argument checks: the bytes from the first element of n rows of
+// `width` elements to past the last one, whether two such ranges share a
+// byte, whether a pointer is not a multiple of an element's size.
+inline long long extent(long long n, long long width, long long ld, int bytes) {
+  return n > 0 && width > 0 ? ((n - 1) * ld + width) * bytes : 0;
+}
+inline bool overlap(const void* a, long long na, const void* b, long long nb) {
+  const char* pa = static_cast<const char*>(a);
+  const char* pb = static_cast<const char*>(b);
+  return na > 0 && nb > 0 && pa < pb + nb && pb < pa + na;
+}
+inline bool misaligned(const void* p, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) != 0;
+}
+
+// E consecutive elements as one aligned access of E * sizeof(T) bytes (a
+// power of two, at most 32: two 16-byte accesses).
+template <class T, int E>
+struct __align__(sizeof(T) * E < 16 ? sizeof(T) * E : 16) Pack {
+  T v[E];
+};
+
+}  // namespace spmv

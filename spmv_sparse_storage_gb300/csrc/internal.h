@@ -81,6 +81,9 @@ int num_sms();
 // error is kept for spmv_last_cuda_error() on this thread and mapped to
 // SPMV_ERR_ALLOC (out of memory) or SPMV_ERR_CUDA.
 int record_cuda(cudaError_t e);
+// SPMV_OK for device (or managed) memory of the current device, else
+// SPMV_ERR_INVALID_ARG (or SPMV_ERR_CUDA when the device cannot be asked).
+int check_current_device_ptrs(const void* const* ptrs, int n);
 
 // ---------------------------------------------------------------------------
 // Launchers. Each returns the cudaError_t of its launches.
@@ -210,6 +213,13 @@ cudaError_t launch_cg_ell_q(int R, int K, const int* ellCol, const float* ellVal
                             CgState* st, cudaStream_t s);
 cudaError_t launch_cg_update(int R, float* X, float* g, const float* d, const float* q,
                              float* partials, CgState* st, cudaStream_t s);
+
+// Stable sort of n tokens (int32 or int64) by their number, those outside
+// 0 .. vocab-1 last (key vocab): *posOut[i] = the token's place in the input,
+// *keyOut[i] = its number, both inside scratch.
+size_t token_sort_scratch_bytes(int n, int vocab);
+cudaError_t launch_token_sort(int n, int vocab, const void* tokens, int indexBytes, void* scratch,
+                              const int** posOut, const int** keyOut, cudaStream_t s);
 
 // items: tail work of the sections wider than kSellMainSlots (nItems of them)
 template <class T>

@@ -1,0 +1,269 @@
+// q4.cu -- matrices of 4-bit codes with a scale per group of a row's columns:
+// conversion from a dense matrix, products with vectors, rows back in dense
+// form.
+#include "dtypes.cuh"
+#include "device_util.cuh"
+#include "internal.h"
+
+namespace spmv {
+namespace {
+
+__device__ __forceinline__ float scale_at(const void* scales, int type, long long i) {
+  switch (type) {
+    case SPMV_F16: return to_f32(static_cast<const __half*>(scales)[i]);
+    case SPMV_BF16: return to_f32(static_cast<const __nv_bfloat16*>(scales)[i]);
+    default: return static_cast<const float*>(scales)[i];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Conversion: one warp per row and group.
+// ---------------------------------------------------------------------------
+template <class W, class S>
+__global__ void __launch_bounds__(256) k_q4_quantize(spmv_q4 a, const W* w, long long ldw,
+                                                     W* back, long long ldb) {
+  const int groups = (a.cols + a.group - 1) / a.group;
+  const long long id = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+  const int lane = threadIdx.x & 31;
+  if (id >= (long long)a.rows * groups) return;
+  const long long r = id / groups;
+  const int gi = (int)(id % groups);
+  const int k0 = gi * a.group, k1 = min(k0 + a.group, a.cols);
+  float v[4];
+  float lo = 0.0f, hi = 0.0f, bad = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int k = k0 + 2 * lane + (j & 1) + 64 * (j >> 1);
+    v[j] = k < k1 ? to_f32(w[r * ldw + k]) : 0.0f;
+    lo = fminf(lo, v[j]);
+    hi = fmaxf(hi, v[j]);
+    if (!(fabsf(v[j]) <= 3.402823466e38f)) bad = 1.0f;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(kFullMask, lo, off));
+    hi = fmaxf(hi, __shfl_xor_sync(kFullMask, hi, off));
+    bad = fmaxf(bad, __shfl_xor_sync(kFullMask, bad, off));
+  }
+  float raw = a.zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f;
+  if (bad != 0.0f) raw = __int_as_float(0x7fc00000);
+  const S held = from_f32<S>(raw);
+  const float step = to_f32(held);
+  const bool usable = step > 0.0f && step <= 3.402823466e38f;
+  float zero = 8.0f;
+  if (a.zeros) zero = usable ? fminf(fmaxf(rintf(-lo / step), 0.0f), 15.0f) : 0.0f;
+  if (lane == 0) {
+    static_cast<S*>(a.scales)[r * a.ld_scales + gi] = held;
+    if (a.zeros) a.zeros[r * a.ld_zeros + gi] = (uint8_t)zero;
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int k = k0 + 2 * lane + 64 * j;
+    if (k >= k1) continue;
+    float q[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      q[i] = usable ? fminf(fmaxf(rintf(v[2 * j + i] / step) + zero, 0.0f), 15.0f) : zero;
+      if (k + i >= k1)
+        q[i] = 0.0f;
+      else if (back)
+        back[r * ldb + k + i] = from_f32<W>((q[i] - zero) * step);
+    }
+    a.codes[r * a.ld_codes + k / 2] = (uint8_t)((int)q[0] | (int)q[1] << 4);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Products: one warp per row and vector.
+// ---------------------------------------------------------------------------
+template <class X, class Y>
+__global__ void __launch_bounds__(256) k_q4_run(spmv_q4 a, int n, const X* __restrict__ x,
+                                                long long ldx, const Y* c, long long ldc, Y* y,
+                                                long long ldy) {
+  const long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+  const int lane = threadIdx.x & 31;
+  if (r >= a.rows) return;
+  for (int j = blockIdx.y; j < n; j += gridDim.y) {
+    float sum = 0.0f;
+    for (int k0 = 0; k0 < a.cols; k0 += a.group) {
+      const int gi = k0 / a.group, k1 = min(k0 + a.group, a.cols);
+      const float zero = a.zeros ? (float)a.zeros[r * a.ld_zeros + gi] : 8.0f;
+      float part = 0.0f;
+      for (int k = k0 + 2 * lane; k < k1; k += 64) {
+        const int b = a.codes[r * a.ld_codes + k / 2];
+        part += ((float)(b & 15) - zero) * to_f32(x[j * ldx + k]);
+        if (k + 1 < k1) part += ((float)(b >> 4) - zero) * to_f32(x[j * ldx + k + 1]);
+      }
+      sum += scale_at(a.scales, a.scale_type, r * a.ld_scales + gi) * part;
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) {
+      if (c) sum += to_f32(c[j * ldc + r]);
+      y[j * ldy + r] = from_f32<Y>(sum);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows back in dense form: one block per token.
+// ---------------------------------------------------------------------------
+template <class O>
+__global__ void __launch_bounds__(256) k_embed_q4(spmv_q4 a, const void* __restrict__ tokens,
+                                                  int wide, float scale, O* __restrict__ out,
+                                                  long long ldo) {
+  const long long t = blockIdx.x;
+  const long long r = !tokens ? t
+                      : wide  ? static_cast<const long long*>(tokens)[t]
+                              : (long long)static_cast<const int*>(tokens)[t];
+  const bool valid = r >= 0 && r < a.rows;
+  for (int k = threadIdx.x; k < a.cols; k += blockDim.x) {
+    float v = 0.0f;
+    if (valid) {
+      const int gi = k / a.group;
+      const int b = a.codes[r * a.ld_codes + k / 2];
+      const float zero = a.zeros ? (float)a.zeros[r * a.ld_zeros + gi] : 8.0f;
+      v = ((float)((k & 1) ? b >> 4 : b & 15) - zero) *
+          scale_at(a.scales, a.scale_type, r * a.ld_scales + gi) * scale;
+    }
+    out[t * ldo + k] = from_f32<O>(v);
+  }
+}
+
+// The host-side checks of a 4-bit matrix: sizes, types and leading dimensions
+// always, the arrays when the matrix is not empty.
+int check_q4(const spmv_q4* a) {
+  if (!a || a->rows < 0 || a->cols < 0 || !dtype_ok(a->scale_type)) return SPMV_ERR_INVALID_ARG;
+  if (a->group != 32 && a->group != 64 && a->group != 128) return SPMV_ERR_INVALID_ARG;
+  const long long groups = ((long long)a->cols + a->group - 1) / a->group;
+  if (a->ld_codes < ((long long)a->cols + 1) / 2 || a->ld_scales < groups)
+    return SPMV_ERR_INVALID_ARG;
+  if (a->zeros && a->ld_zeros < groups) return SPMV_ERR_INVALID_ARG;
+  if (a->rows == 0 || a->cols == 0) return SPMV_OK;
+  if (!a->codes || !a->scales || misaligned(a->scales, dtype_bytes(a->scale_type)))
+    return SPMV_ERR_INVALID_ARG;
+  return SPMV_OK;
+}
+
+}  // namespace
+}  // namespace spmv
+
+extern "C" {
+
+int spmv_q4_quantize(const spmv_q4* a, spmv_dtype wType, const void* d_w, int64_t ldw,
+                     void* d_back, int64_t ld_back, void* stream) {
+  using namespace spmv;
+  int st = check_q4(a);
+  if (st != SPMV_OK) return st;
+  if (!dtype_ok(wType) || ldw < a->cols || (d_back && ld_back < a->cols))
+    return SPMV_ERR_INVALID_ARG;
+  if (a->rows == 0 || a->cols == 0) return SPMV_OK;
+  const int wb = dtype_bytes(wType);
+  if (!d_w || misaligned(d_w, wb) || misaligned(d_back, wb)) return SPMV_ERR_INVALID_ARG;
+  const long long groups = ((long long)a->cols + a->group - 1) / a->group;
+  const void* arr[] = {d_w, a->codes, a->scales, d_back, a->zeros};
+  const long long len[] = {extent(a->rows, a->cols, ldw, wb),
+                           extent(a->rows, ((long long)a->cols + 1) / 2, a->ld_codes, 1),
+                           extent(a->rows, groups, a->ld_scales, dtype_bytes(a->scale_type)),
+                           d_back ? extent(a->rows, a->cols, ld_back, wb) : 0,
+                           a->zeros ? extent(a->rows, groups, a->ld_zeros, 1) : 0};
+  for (int i = 0; i < 5; ++i)
+    for (int j = i + 1; j < 5; ++j)
+      if (overlap(arr[i], len[i], arr[j], len[j]) &&
+          !(i == 0 && j == 3 && d_back == d_w && ld_back == ldw))
+        return SPMV_ERR_INVALID_ARG;
+  st = check_current_device_ptrs(arr, 5);
+  if (st != SPMV_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const long long warps = a->rows * groups;
+  if ((warps + 7) / 8 > 0x7fffffffLL) return SPMV_ERR_TOO_LARGE;
+  return record_cuda(with_dtype(wType, [&](auto wv) {
+    return with_dtype(a->scale_type, [&](auto sv) {
+      using W = decltype(wv);
+      using S = decltype(sv);
+      k_q4_quantize<W, S><<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(
+          *a, static_cast<const W*>(d_w), ldw, static_cast<W*>(d_back), ld_back);
+      note_launches(1);
+      return cudaGetLastError();
+    });
+  }));
+}
+
+int spmv_q4_run(const spmv_q4* a, int32_t n, spmv_dtype xType, const void* d_x, int64_t ldx,
+                const void* d_c, int64_t ldc, spmv_dtype yType, void* d_y, int64_t ldy,
+                void* stream) {
+  using namespace spmv;
+  int st = check_q4(a);
+  if (st != SPMV_OK) return st;
+  if (n < 0 || !dtype_ok(xType) || !dtype_ok(yType)) return SPMV_ERR_INVALID_ARG;
+  if (ldx < a->cols || ldy < a->rows || (d_c && ldc < a->rows)) return SPMV_ERR_INVALID_ARG;
+  if (n == 0 || a->rows == 0) return SPMV_OK;
+  const int xb = dtype_bytes(xType), yb = dtype_bytes(yType);
+  if (!d_y || (a->cols > 0 && !d_x)) return SPMV_ERR_INVALID_ARG;
+  if (misaligned(d_x, xb) || misaligned(d_y, yb) || misaligned(d_c, yb))
+    return SPMV_ERR_INVALID_ARG;
+  const long long yLen = extent(n, a->rows, ldy, yb);
+  const long long groups = ((long long)a->cols + a->group - 1) / a->group;
+  if (overlap(d_y, yLen, d_x, extent(n, a->cols, ldx, xb)) ||
+      overlap(d_y, yLen, a->codes,
+              extent(a->rows, ((long long)a->cols + 1) / 2, a->ld_codes, 1)) ||
+      overlap(d_y, yLen, a->scales,
+              extent(a->rows, groups, a->ld_scales, dtype_bytes(a->scale_type))) ||
+      (a->zeros && overlap(d_y, yLen, a->zeros, extent(a->rows, groups, a->ld_zeros, 1))))
+    return SPMV_ERR_INVALID_ARG;
+  if (d_c && !(d_c == d_y && ldc == ldy) && overlap(d_y, yLen, d_c, extent(n, a->rows, ldc, yb)))
+    return SPMV_ERR_INVALID_ARG;
+  const void* ptrs[] = {a->cols > 0 ? a->codes : nullptr, a->cols > 0 ? a->scales : nullptr,
+                        a->cols > 0 ? a->zeros : nullptr, a->cols > 0 ? d_x : nullptr, d_c, d_y};
+  st = check_current_device_ptrs(ptrs, 6);
+  if (st != SPMV_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return record_cuda(with_dtype(xType, [&](auto xv) {
+    return with_dtype(yType, [&](auto yv) {
+      using X = decltype(xv);
+      using Y = decltype(yv);
+      const dim3 grid((unsigned)(((long long)a->rows + 7) / 8), (unsigned)(n < 64 ? n : 64));
+      k_q4_run<X, Y><<<grid, 256, 0, s>>>(*a, n, static_cast<const X*>(d_x), ldx,
+                                          static_cast<const Y*>(d_c), ldc, static_cast<Y*>(d_y),
+                                          ldy);
+      note_launches(1);
+      return cudaGetLastError();
+    });
+  }));
+}
+
+int spmv_embed_q4(const spmv_q4* a, int32_t nTokens, int32_t indexBytes, const void* d_tokens,
+                  float scale, spmv_dtype outType, void* d_out, int64_t ld_out, void* stream) {
+  using namespace spmv;
+  int st = check_q4(a);
+  if (st != SPMV_OK) return st;
+  if (nTokens < 0 || !dtype_ok(outType) || ld_out < a->cols) return SPMV_ERR_INVALID_ARG;
+  if (indexBytes != 4 && indexBytes != 8) return SPMV_ERR_INVALID_ARG;
+  if (nTokens == 0 || a->cols == 0) return SPMV_OK;
+  const int ob = dtype_bytes(outType);
+  if (!d_out || misaligned(d_out, ob) || misaligned(d_tokens, indexBytes))
+    return SPMV_ERR_INVALID_ARG;
+  if (!d_tokens && nTokens > a->rows) return SPMV_ERR_INVALID_ARG;
+  const long long oLen = extent(nTokens, a->cols, ld_out, ob);
+  const long long groups = ((long long)a->cols + a->group - 1) / a->group;
+  if (overlap(d_out, oLen, a->codes,
+              extent(a->rows, ((long long)a->cols + 1) / 2, a->ld_codes, 1)) ||
+      overlap(d_out, oLen, a->scales,
+              extent(a->rows, groups, a->ld_scales, dtype_bytes(a->scale_type))) ||
+      (a->zeros && overlap(d_out, oLen, a->zeros, extent(a->rows, groups, a->ld_zeros, 1))) ||
+      (d_tokens && overlap(d_out, oLen, d_tokens, (long long)nTokens * indexBytes)))
+    return SPMV_ERR_INVALID_ARG;
+  const void* ptrs[] = {a->rows > 0 ? a->codes : nullptr, a->rows > 0 ? a->scales : nullptr,
+                        a->rows > 0 ? a->zeros : nullptr, d_tokens, d_out};
+  st = check_current_device_ptrs(ptrs, 5);
+  if (st != SPMV_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return record_cuda(with_dtype(outType, [&](auto ov) {
+    using O = decltype(ov);
+    k_embed_q4<O><<<(unsigned)nTokens, 256, 0, s>>>(*a, d_tokens, indexBytes == 8, scale,
+                                                    static_cast<O*>(d_out), ld_out);
+    note_launches(1);
+    return cudaGetLastError();
+  }));
+}
+
+}  // extern "C"
