@@ -20,7 +20,8 @@ LIB = os.path.join(LIB_DIR, "libspmv_gb300.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "stats.cu", "convert.cu", "ell_convert.cu", "spmv_kernels.cu", "noalloc.cu",
-           "cg.cu", "q4.cu", "embed.cu"]
+           "cg.cu", "q4.cu",
+           "q4_run_f32.cu", "q4_run_f16.cu", "q4_run_bf16.cu", "embed.cu"]
 
 
 def nvcc() -> str:

@@ -4,6 +4,7 @@
 #include "dtypes.cuh"
 #include "device_util.cuh"
 #include "internal.h"
+#include "q4.h"
 
 namespace spmv {
 namespace {
@@ -74,37 +75,6 @@ __global__ void __launch_bounds__(256) k_q4_quantize(spmv_q4 a, const W* w, long
 }
 
 // ---------------------------------------------------------------------------
-// Products: one warp per row and vector.
-// ---------------------------------------------------------------------------
-template <class X, class Y>
-__global__ void __launch_bounds__(256) k_q4_run(spmv_q4 a, int n, const X* __restrict__ x,
-                                                long long ldx, const Y* c, long long ldc, Y* y,
-                                                long long ldy) {
-  const long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x & 31;
-  if (r >= a.rows) return;
-  for (int j = blockIdx.y; j < n; j += gridDim.y) {
-    float sum = 0.0f;
-    for (int k0 = 0; k0 < a.cols; k0 += a.group) {
-      const int gi = k0 / a.group, k1 = min(k0 + a.group, a.cols);
-      const float zero = a.zeros ? (float)a.zeros[r * a.ld_zeros + gi] : 8.0f;
-      float part = 0.0f;
-      for (int k = k0 + 2 * lane; k < k1; k += 64) {
-        const int b = a.codes[r * a.ld_codes + k / 2];
-        part += ((float)(b & 15) - zero) * to_f32(x[j * ldx + k]);
-        if (k + 1 < k1) part += ((float)(b >> 4) - zero) * to_f32(x[j * ldx + k + 1]);
-      }
-      sum += scale_at(a.scales, a.scale_type, r * a.ld_scales + gi) * part;
-    }
-    sum = warp_sum(sum);
-    if (lane == 0) {
-      if (c) sum += to_f32(c[j * ldc + r]);
-      y[j * ldy + r] = from_f32<Y>(sum);
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
 // Rows back in dense form: one block per token.
 // ---------------------------------------------------------------------------
 template <class O>
@@ -145,6 +115,72 @@ int check_q4(const spmv_q4* a) {
 }
 
 }  // namespace
+}  // namespace spmv
+
+namespace spmv {
+namespace q4 {
+
+// The split of a launch. The grid is one wave of resident blocks where the
+// tiles allow it; P, the blocks that share a tile's columns, is the one whose
+// slowest block has the least to do, counted in steps per warp.
+Plan make_plan(const RunArgs& p, int tileRows, int columns, int ringBytes) {
+  constexpr int kXBytes = 64 * 1024;    // x staged at a time
+  constexpr int kSumBytes = 24 * 1024;  // partial sums held at a time
+  constexpr int kFill = 6;              // steps that a wave's start and end cost
+  Plan best{};
+  long long bestCost = -1;
+  const long long tiles = ((long long)p.a.rows + tileRows - 1) / tileRows;
+  const int steps = (int)(((long long)p.a.cols + 127) / 128);
+  const int perStep = columns * 256;           // x bytes of a step
+  const int slot = tileRows * columns * 4;     // partial sums of a tile and warp
+  const int tileSum = tileRows * p.n * 4;
+  for (int P = 1; P <= 8 && P <= (steps > 0 ? steps : 1); P *= 2) {
+    Plan c{};
+    c.P = P;
+    c.tiles = tiles;
+    c.steps = steps;
+    const int own = steps > 0 ? (steps + P - 1) / P : 1;
+    c.phaseSteps = own;
+    while (c.phaseSteps > 1 && (long long)c.phaseSteps * perStep > kXBytes)
+      c.phaseSteps = (c.phaseSteps + 1) / 2;
+    const bool sums = P > 1 || c.phaseSteps < own;
+    long long room = (kSumBytes - (long long)kWarps * slot) / (slot + (sums ? tileSum : 0));
+    if (room < 1) room = 1;
+    const int fixed = ringBytes + c.phaseSteps * perStep + 1024;
+    const int most = fixed + kSumBytes;
+    int resident = kMaxSmem / most;
+    if (resident < 1) resident = 1;
+    if (resident > 2) resident = 2;  // by registers
+    const long long slots = (long long)num_sms() * resident / P;
+    long long waves = (tiles + slots * room - 1) / (slots * room);
+    if (waves < 1) waves = 1;
+    c.clusters = slots * waves < tiles ? slots * waves : tiles;
+    if (c.clusters < 1) c.clusters = 1;
+    c.maxTiles = (int)((tiles + c.clusters - 1) / c.clusters);
+    const long long units = ((long long)c.maxTiles * own + kWarps - 1) / kWarps;
+    const long long cost = waves * (units + kFill) + (P > 1 ? 4 : 0);
+    c.smem = (size_t)ringBytes + (size_t)c.phaseSteps * perStep +
+             (size_t)(c.maxTiles + kWarps) * slot + (sums ? (size_t)c.maxTiles * tileSum : 0);
+    if (bestCost < 0 || cost < bestCost) {
+      bestCost = cost;
+      best = c;
+    }
+  }
+  return best;
+}
+
+cudaError_t SmemOnce::allow(const void* kernel) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+}  // namespace q4
 }  // namespace spmv
 
 extern "C" {
@@ -217,17 +253,26 @@ int spmv_q4_run(const spmv_q4* a, int32_t n, spmv_dtype xType, const void* d_x, 
   st = check_current_device_ptrs(ptrs, 6);
   if (st != SPMV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  q4::RunArgs r{};
+  r.a = *a;
+  r.codesEnd = a->codes + extent(a->rows, ((long long)a->cols + 1) / 2, a->ld_codes, 1);
+  r.ldx = ldx;
+  r.xVec = aligned16(d_x) && (n == 1 || ldx * xb % 16 == 0);
+  r.ldc = ldc;
+  r.yType = yType;
+  r.ldy = ldy;
   return record_cuda(with_dtype(xType, [&](auto xv) {
-    return with_dtype(yType, [&](auto yv) {
-      using X = decltype(xv);
-      using Y = decltype(yv);
-      const dim3 grid((unsigned)(((long long)a->rows + 7) / 8), (unsigned)(n < 64 ? n : 64));
-      k_q4_run<X, Y><<<grid, 256, 0, s>>>(*a, n, static_cast<const X*>(d_x), ldx,
-                                          static_cast<const Y*>(d_c), ldc, static_cast<Y*>(d_y),
-                                          ldy);
-      note_launches(1);
-      return cudaGetLastError();
-    });
+    using X = decltype(xv);
+    constexpr int most = q4::vectors_per_pass<X>();
+    for (int j = 0; j < n; j += most) {
+      r.n = n - j < most ? n - j : most;
+      r.x = static_cast<const X*>(d_x) + j * ldx;
+      r.y = static_cast<char*>(d_y) + j * ldy * yb;
+      r.c = d_c ? static_cast<const char*>(d_c) + j * ldc * yb : nullptr;
+      const cudaError_t e = q4::launch_run<X>(r, s);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
   }));
 }
 
