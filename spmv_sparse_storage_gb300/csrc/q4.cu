@@ -120,64 +120,103 @@ int check_q4(const spmv_q4* a) {
 namespace spmv {
 namespace q4 {
 
-// The split of a launch. The grid is one wave of resident blocks where the
-// tiles allow it; P, the blocks that share a tile's columns, is the one whose
-// slowest block has the least to do, counted in steps per warp.
-Plan make_plan(const RunArgs& p, int tileRows, int columns, int ringBytes) {
-  constexpr int kXBytes = 64 * 1024;    // x staged at a time
-  constexpr int kSumBytes = 24 * 1024;  // partial sums held at a time
-  constexpr int kFill = 6;              // steps that a wave's start and end cost
+// The split of a launch: P, the blocks that share a tile's columns, and the
+// blocks on an SM, whose cost by this model is the least. In tenths of a
+// microsecond, fitted to 8 shapes from 1024 x 1024 to 131072 x 4096: a warp's
+// step takes 20 with two blocks on an SM and 14 with one, bringing 4 KB of x
+// into shared memory 4, a phase's start 30, a join across the cluster 4 + 2 P
+// (8192 x 28672 with one bf16 vector: P = 4 with two blocks 29.5 us, P = 1
+// 37.0, one block 43.8; 1024 x 1024: P = 1 4.0, P = 2 4.6; 600 x 16384 with
+// two vectors: P = 8 6.2, P = 1 18.0).
+Plan make_plan(const RunArgs& p, int columns, int stepCols, int ringBytes, const Residency& res) {
   Plan best{};
   long long bestCost = -1;
-  const long long tiles = ((long long)p.a.rows + tileRows - 1) / tileRows;
-  const int steps = (int)(((long long)p.a.cols + 127) / 128);
-  const int perStep = columns * 256;           // x bytes of a step
-  const int slot = tileRows * columns * 4;     // partial sums of a tile and warp
-  const int tileSum = tileRows * p.n * 4;
-  for (int P = 1; P <= 8 && P <= (steps > 0 ? steps : 1); P *= 2) {
-    Plan c{};
-    c.P = P;
-    c.tiles = tiles;
-    c.steps = steps;
-    const int own = steps > 0 ? (steps + P - 1) / P : 1;
-    c.phaseSteps = own;
-    while (c.phaseSteps > 1 && (long long)c.phaseSteps * perStep > kXBytes)
-      c.phaseSteps = (c.phaseSteps + 1) / 2;
-    const bool sums = P > 1 || c.phaseSteps < own;
-    long long room = (kSumBytes - (long long)kWarps * slot) / (slot + (sums ? tileSum : 0));
-    if (room < 1) room = 1;
-    const int fixed = ringBytes + c.phaseSteps * perStep + 1024;
-    const int most = fixed + kSumBytes;
-    int resident = kMaxSmem / most;
-    if (resident < 1) resident = 1;
-    if (resident > 2) resident = 2;  // by registers
-    const long long slots = (long long)num_sms() * resident / P;
-    long long waves = (tiles + slots * room - 1) / (slots * room);
-    if (waves < 1) waves = 1;
-    c.clusters = slots * waves < tiles ? slots * waves : tiles;
-    if (c.clusters < 1) c.clusters = 1;
-    c.maxTiles = (int)((tiles + c.clusters - 1) / c.clusters);
-    const long long units = ((long long)c.maxTiles * own + kWarps - 1) / kWarps;
-    const long long cost = waves * (units + kFill) + (P > 1 ? 4 : 0);
-    c.smem = (size_t)ringBytes + (size_t)c.phaseSteps * perStep +
-             (size_t)(c.maxTiles + kWarps) * slot + (sums ? (size_t)c.maxTiles * tileSum : 0);
-    if (bestCost < 0 || cost < bestCost) {
-      bestCost = cost;
-      best = c;
+  const long long tiles = ((long long)p.a.rows + kTileRows - 1) / kTileRows;
+  const int steps = (int)(((long long)p.a.cols + stepCols - 1) / stepCols);
+  const int perStep = columns * stepCols * 2;  // x bytes of a step
+  const int slot = kTileRows * columns * 4;    // partial sums of a tile and warp
+  const int tileSum = kTileRows * p.n * 4;
+  for (int i = 0; i < 4 && (1 << i) <= (steps > 0 ? steps : 1); ++i) {
+    for (int onSm = 1; onSm <= 2; ++onSm) {
+      Plan c{};
+      c.P = 1 << i;
+      c.logP = i;
+      c.tiles = tiles;
+      c.steps = steps;
+      const int own = steps > 0 ? (steps + c.P - 1) / c.P : 1;
+      const long long atOnce = res.clusters[i][onSm - 1];
+      if (atOnce < 1) continue;
+      // a block's shared memory: its share of an SM's, less the 1 KB that each
+      // takes for itself; x in as few phases of equal length as there is room for
+      const long long room = (kMaxSmem + 1024) / onSm - 1024 - ringBytes -
+                             (long long)(kWarps - 1) * slot;
+      long long tilesEach = (tiles + atOnce - 1) / atOnce;
+      int phases = 1;
+      for (;; ++phases) {
+        c.phaseSteps = (own + phases - 1) / phases;
+        const long long perTile = slot + (phases > 1 ? tileSum : 0);
+        const long long left = room - (long long)c.phaseSteps * perStep;
+        if (left >= perTile && (left >= tilesEach * perTile || phases >= 4 || c.phaseSteps == 1)) {
+          if (left < tilesEach * perTile) tilesEach = left / perTile;
+          break;
+        }
+        if (c.phaseSteps == 1) {
+          tilesEach = 0;
+          break;
+        }
+      }
+      if (tilesEach < 1) continue;
+      const long long waves = (tiles + atOnce * tilesEach - 1) / (atOnce * tilesEach);
+      c.clusters = atOnce * waves < tiles ? atOnce * waves : tiles;
+      if (c.clusters < 1) c.clusters = 1;
+      c.maxTiles = (int)((tiles + c.clusters - 1) / c.clusters);
+      c.smem = (size_t)ringBytes + (size_t)c.phaseSteps * perStep +
+               (size_t)(c.maxTiles + kWarps - 1) * slot +
+               (phases > 1 ? (size_t)c.maxTiles * tileSum : 0);
+      const long long units = ((long long)c.maxTiles * own + kWarps - 1) / kWarps;
+      const long long fetches = ((long long)own * perStep + 4095) / 4096;
+      const long long cost =
+          waves * (units * (onSm == 1 ? 14 : 20) + fetches * 4 + phases * 30) +
+          (c.P > 1 ? 4 + 2 * c.P : 0);
+      if (bestCost < 0 || cost < bestCost) {
+        bestCost = cost;
+        best = c;
+      }
     }
   }
   return best;
 }
 
-cudaError_t SmemOnce::allow(const void* kernel) {
+cudaError_t Residency::ask(const void* kernel) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  if (devices.load(std::memory_order_acquire) & bit) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
+  if (e != cudaSuccess) return e;
+  for (int i = 0; i < 4; ++i)
+    for (int m = 0; m < 2; ++m) {
+      int n = num_sms() * (m + 1);
+      if (i > 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(n >> i << i));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = (kMaxSmem + 1024) / (m + 1) - 1024;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1u << i;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (e != cudaSuccess) return e;
+      }
+      clusters[i][m] = n;
+    }
+  devices.fetch_or(bit, std::memory_order_release);
+  return cudaSuccess;
 }
 
 }  // namespace q4

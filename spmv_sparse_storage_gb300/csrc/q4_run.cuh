@@ -16,9 +16,9 @@
 // time either way, and operands go from the code words to the instruction in
 // registers, without a second trip through shared memory.
 //
-// Layout. A tile is 16 * MT rows; a step is 128 columns of it. Each warp brings
-// its steps into a ring of kStages buffers of its own by asynchronous 16-byte
-// copies (64 bytes per row), so no barrier is taken between steps. Lane (g, c),
+// Layout. A tile is 32 rows; a step is 256 columns of it, 4 KB. Each warp
+// brings its steps into a ring of kStages buffers of its own by asynchronous
+// 16-byte copies, so no barrier is taken between steps. Lane (g, c),
 // g = lane / 4 and c = lane % 4, holds columns c * G/4 .. of each group of rows g
 // and g + 8 (of each 16): any assignment of columns to the k index of an mma is
 // as good as another when A and x agree, and this one keeps a group in one mma
@@ -45,22 +45,20 @@ namespace spmv {
 namespace q4 {
 
 // --- pieces --------------------------------------------------------------------
-__device__ __forceinline__ void mma16816(float (&d)[4], const unsigned (&a)[4], unsigned b0,
-                                         unsigned b1, __half) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], const unsigned (&a)[4], unsigned b0,
-                                         unsigned b1, __nv_bfloat16) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
+// d = A B + c (16 x 16 by 16 x 8)
+#define SPMV_MMA16816(TYPE, NAME)                                                              \
+  __device__ __forceinline__ void mma16816(float (&d)[4], const unsigned (&a)[4], unsigned b0, \
+                                           unsigned b1, float c0, float c1, float c2, float c3,\
+                                           TYPE) {                                             \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." NAME "." NAME                                 \
+        ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"                       \
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                       \
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1),      \
+          "f"(c2), "f"(c3));                                                                   \
+  }
+SPMV_MMA16816(__half, "f16")
+SPMV_MMA16816(__nv_bfloat16, "bf16")
+#undef SPMV_MMA16816
 
 // A 16-bit operand type: the magic word m such that m | q (q < 128) is base + q
 // exactly, and the packed difference.
@@ -98,19 +96,57 @@ struct OpOf<__nv_bfloat16> {
   static constexpr int kParts = 1;
 };
 
-// entries j and j + 4 of a code word, less their zero point (bias = magic | z)
+// entries j and j + 4 of a code word, less their zero point (bias = magic | z).
+// magic and mask come in registers: as constants they made two instructions of
+// the one that masks and sets (8192 x 28672: 113 -> 83 ALU instructions for 16
+// rows of 128 columns, 45.7 -> 41.6 us).
 template <class Op>
-__device__ __forceinline__ unsigned unpack(unsigned w, int j, unsigned bias) {
-  return Op::sub(((w >> (4 * j)) & 0x000f000fu) | Op::kMagic, bias);
+__device__ __forceinline__ unsigned unpack(unsigned w, int j, unsigned mask, unsigned magic,
+                                           unsigned bias) {
+  unsigned v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * j)), "r"(mask), "r"(magic));
+  return Op::sub(v, bias);
+}
+__device__ __forceinline__ unsigned in_register(unsigned v) {
+  asm volatile("" : "+r"(v));
+  return v;
 }
 
 // 16-byte asynchronous copy of the first `bytes` (1 .. 16) of a 16-byte chunk,
 // zeros in the rest.
-__device__ __forceinline__ void cp_async16_part(void* smem, const void* gmem, int bytes) {
-  const unsigned sa = (unsigned)__cvta_generic_to_shared(smem);
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(sa), "l"(gmem),
+__device__ __forceinline__ void cp_async16_part(unsigned smem, const void* gmem, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem),
                "r"(bytes)
                : "memory");
+}
+__device__ __forceinline__ void cp_async16(unsigned smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(smem), "l"(gmem)
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+// Shared memory by its own 32-bit addresses (the ring and the staged x).
+__device__ __forceinline__ unsigned lds32(unsigned a) {
+  unsigned v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(unsigned a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(unsigned a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts8(unsigned a, unsigned v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -120,18 +156,17 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Chunk position inside a row's 64 bytes: rows 2 apart are moved so that the
-// lanes' 4-, 8- and 16-byte reads of 8 rows fall into different banks.
+// Where 16-byte chunk j of a row's ROW bytes (64 or 128) is kept: moved so that
+// the lanes' 4-, 8- and 16-byte reads of 8 rows fall into different banks.
+template <int ROW>
 __device__ __forceinline__ int chunk_at(int row, int j) {
-  const int p = (row >> 1) & 3;
-  return j ^ (((p & 1) << 1) | (p >> 1));
+  if (ROW == 128) return j ^ (((row & 1) << 2) | (row & 2) | ((row >> 2) & 1));
+  return j ^ ((row & 2) | ((row >> 2) & 1));
 }
 
-// The 16-bit operands of 8 consecutive columns k .. k + 7 of one vector, in the
-// order 0 4 1 5 2 6 3 7, one word per pair; part 0, 1 or 2 of an fp32 vector.
+// 8 consecutive entries of a vector, zeros past its end.
 template <class X>
-__device__ __forceinline__ void stage_x(const X* x, long long k, long long cols, bool vec,
-                                        uint4* out, int stride) {
+__device__ __forceinline__ Pack<X, 8> fetch_x(const X* x, long long k, long long cols, bool vec) {
   Pack<X, 8> v;
   if (vec && k + 8 <= cols) {
     v = *reinterpret_cast<const Pack<X, 8>*>(x + k);
@@ -139,30 +174,31 @@ __device__ __forceinline__ void stage_x(const X* x, long long k, long long cols,
 #pragma unroll
     for (int i = 0; i < 8; ++i) v.v[i] = k + i < cols ? x[k + i] : from_f32<X>(0.0f);
   }
+  return v;
+}
+__device__ __forceinline__ uint4 in_operand_order(const unsigned (&h)[8]) {
+  return make_uint4(h[0] | h[4] << 16, h[1] | h[5] << 16, h[2] | h[6] << 16, h[3] | h[7] << 16);
+}
+// Their 16-bit operands in the order 0 4 1 5 2 6 3 7; an fp32 vector's three
+// parts go to three columns (4 pieces apart).
+template <class X>
+__device__ __forceinline__ void stage_x(const Pack<X, 8>& v, uint4* out) {
   unsigned h[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) h[i] = *reinterpret_cast<const unsigned short*>(&v.v[i]);
-  *out = make_uint4(h[0] | h[4] << 16, h[1] | h[5] << 16, h[2] | h[6] << 16, h[3] | h[7] << 16);
+  *out = in_operand_order(h);
 }
 template <>
-__device__ __forceinline__ void stage_x<float>(const float* x, long long k, long long cols,
-                                               bool vec, uint4* out, int stride) {
+__device__ __forceinline__ void stage_x<float>(const Pack<float, 8>& in, uint4* out) {
   float v[8];
-  if (vec && k + 8 <= cols) {
-    const float4 a = *reinterpret_cast<const float4*>(x + k);
-    const float4 b = *reinterpret_cast<const float4*>(x + k + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = k + i < cols ? x[k + i] : 0.0f;
-  }
+  for (int i = 0; i < 8; ++i) v[i] = in.v[i];
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
     unsigned h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      unsigned bits = __float_as_uint(v[i]);
+      const unsigned bits = __float_as_uint(v[i]);
       if ((bits & 0x7f800000u) == 0x7f800000u) {
         // an infinity or a NaN is its first part alone (a NaN kept one by a bit)
         h[i] = (bits >> 16) | ((bits & 0x007fffffu) ? 0x40u : 0u);
@@ -172,19 +208,15 @@ __device__ __forceinline__ void stage_x<float>(const float* x, long long k, long
         v[i] -= __uint_as_float(bits & 0xffff0000u);
       }
     }
-    out[p * stride] =
-        make_uint4(h[0] | h[4] << 16, h[1] | h[5] << 16, h[2] | h[6] << 16, h[3] | h[7] << 16);
+    out[p * 4] = in_operand_order(h);
   }
 }
 
-__device__ __forceinline__ float scale_value(unsigned raw, int type) {
-  if (type == SPMV_F32) return __uint_as_float(raw);
-  if (type == SPMV_BF16) return __uint_as_float(raw << 16);
-  return __half2float(__ushort_as_half((unsigned short)raw));
-}
-__device__ __forceinline__ unsigned scale_raw(const void* scales, int type, long long i) {
-  return type == SPMV_F32 ? __ldg(static_cast<const unsigned*>(scales) + i)
-                          : (unsigned)__ldg(static_cast<const unsigned short*>(scales) + i);
+// A scale from its bits: fp32 (shift 0), bf16 (shift 16) or fp16.
+__device__ __forceinline__ float scale_value(unsigned raw, int shift, bool half) {
+  float f = __uint_as_float(raw << shift);
+  if (half) f = __half2float(__ushort_as_half((unsigned short)raw));
+  return f;
 }
 __device__ __forceinline__ float load_y(const void* p, int type, long long i) {
   return type == SPMV_F32   ? static_cast<const float*>(p)[i]
@@ -200,237 +232,377 @@ __device__ __forceinline__ void store_y(void* p, int type, long long i, float v)
     static_cast<__nv_bfloat16*>(p)[i] = from_f32<__nv_bfloat16>(v);
 }
 
+// The warp that holds unit u of `units` divided among the warps (units: tiles and
+// steps of which shared memory holds the sums and the x, so well below 2^24).
+__device__ __forceinline__ int owner(int u, int units) {
+  return ((u + 1) * kWarps - 1) / units;
+}
+
 // --- the kernel ------------------------------------------------------------------
 // ALIGNED: every row of codes starts on a 16-byte boundary. Otherwise a row's
-// 64 bytes are fetched as the (at most) 5 aligned chunks that hold them and
-// shifted into place when read.
-template <class X, int G, int NT, int MT, bool ALIGNED>
+// bytes are fetched as the aligned chunks that hold them, one more than they
+// would fill, and shifted into place when read.
+// ZEROS: the matrix has zero points.
+template <class X, int G, int NT, bool ALIGNED, bool ZEROS>
 __global__ void __launch_bounds__(kThreads, 2) k_q4_run(const RunArgs p) {
   using Op = typename OpOf<X>::Op;
+  using OpT = typename Op::T;
   constexpr int kParts = OpOf<X>::kParts;
-  constexpr int kRowBytes = ALIGNED ? 64 : 80;
-  constexpr int kStep = 16 * MT * kRowBytes;  // bytes of a stage
-  constexpr int kGroups = 128 / G;            // groups of a step
-  constexpr int kWords = G / 32;              // code words of a lane, row and group
+  constexpr int kStepCols = kStepColsOf<NT>;
+  constexpr int kStages = kStagesOf<NT>;
+  constexpr int kRow = kStepCols / 2;             // code bytes of a row and step
+  constexpr int kPitch = ALIGNED ? kRow : kRow + 16;
+  constexpr int kStep = kTileRows * kPitch;       // bytes of a stage
+  constexpr int kGroups = kStepCols / G;          // groups of a step
+  constexpr int kWords = G / 32;                  // code words of a lane, row and group
+  constexpr int kStepWords = kStepCols / 32;      // of a lane, row and step
+  constexpr int kRows = kTileRows / 8;            // rows of a lane: g, g + 8, g + 16, g + 24
+  // the scales that a lane fetches for the four lanes of its rows: of sRows
+  // rows from row sRow0 on and sGroups groups from group sGroup0 on
+  constexpr int sRows = kGroups < 4 ? kGroups : 4, sGroups = kGroups < 8 ? 1 : 2;
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   const spmv_q4& a = p.a;
   const int NB = p.n * kParts;  // columns
-  unsigned char* ring = smem + warp * kStages * kStep;
+  const unsigned smem0 = (unsigned)__cvta_generic_to_shared(smem);
+  const unsigned ring = smem0 + warp * kStages * kStep;
+  const unsigned xs0 = smem0 + kWarps * kStages * kStep;
   uint4* xs = reinterpret_cast<uint4*>(smem + kWarps * kStages * kStep);
-  float* slots = reinterpret_cast<float*>(xs + (size_t)p.phaseSteps * 16 * NB);
-  const int slotFloats = 16 * MT * NB;
-  float* sums = slots + (size_t)(p.maxTiles + kWarps) * slotFloats;
+  float* slots = reinterpret_cast<float*>(xs + (size_t)p.phaseSteps * (kStepCols / 8) * NB);
+  const int slotFloats = kTileRows * NB;
+  const unsigned mask = in_register(0x000f000fu), magic = in_register(Op::kMagic);
 
-  const int rank = blockIdx.x % p.P;
-  const long long cluster = blockIdx.x / p.P, clusters = gridDim.x / p.P;
-  const int t0 = (int)(p.tiles * cluster / clusters);
-  const int T = (int)(p.tiles * (cluster + 1) / clusters) - t0;
-  const int s0 = (int)((long long)p.steps * rank / p.P);
-  const int s1 = (int)((long long)p.steps * (rank + 1) / p.P);
-  const long long rowBytes = ((long long)a.cols + 1) / 2;
+  // this cluster's tiles and this block's steps: equal shares, the first ones
+  // one more where they do not divide
+  const int rank = p.P > 1 ? blockIdx.x & (p.P - 1) : 0;
+  const int cluster = blockIdx.x >> p.logP;
+  const int t0 = cluster * p.tileShare + min(cluster, p.tileRest);
+  const int T = p.tileShare + (cluster < p.tileRest ? 1 : 0);
+  const int s0 = rank * p.stepShare + min(rank, p.stepRest);
+  const int s1 = s0 + p.stepShare + (rank < p.stepRest ? 1 : 0);
+  // sums of the phases so far, where there are several
+  float* sums = slots + (size_t)(p.maxTiles + kWarps - 1) * slotFloats;
+  const int xWord4 = NB * 4;  // 16-byte pieces of x from one code word to the next
+  const bool phases = p.phaseSteps < p.stepShare + (p.stepRest > 0 ? 1 : 0);
+  const int rowBytes = a.cols / 2 + a.cols % 2;
   const int groups = (a.cols + G - 1) / G;
   const X* x = static_cast<const X*>(p.x);
-  const int outs = T * 16 * MT * p.n;
+  const int scaleBytes = a.scale_type == SPMV_F32 ? 4 : 2;
+  const int scaleShift = a.scale_type == SPMV_BF16 ? 16 : 0;
+  const bool scaleHalf = a.scale_type == SPMV_F16;
+  const long long rows8 = 8 * a.ld_codes, scales8 = 8 * a.ld_scales * scaleBytes,
+                  zeros8 = 8 * a.ld_zeros;
+  const int sRow0 = kGroups == 1 ? c : kGroups == 2 ? 2 * (c & 1) : 0;
+  const int sGroup0 = kGroups == 1 ? 0 : kGroups == 2 ? c >> 1 : kGroups == 4 ? c : 2 * c;
+  // where the lane's chunks of row g go in a stage, and where its codes of a
+  // group and row g are (row g + 8 i: 8 i * kPitch further on)
+  unsigned put[kRow / 64];
+#pragma unroll
+  for (int j = 0; j < kRow / 64; ++j)
+    put[j] = ring + g * kPitch + chunk_at<kRow>(g, c + 4 * j) * 16;
+  unsigned get[kGroups];
+#pragma unroll
+  for (int gr = 0; gr < kGroups; ++gr) {
+    const int byte = gr * (G / 2) + c * (G / 8);
+    get[gr] = ring + g * kPitch + chunk_at<kRow>(g, byte >> 4) * 16 + (byte & 15);
+  }
 
   for (int f0 = s0; f0 == s0 || f0 < s1; f0 += p.phaseSteps) {
     const int fs = min(p.phaseSteps, s1 - f0);  // steps of this phase (0: no columns)
     const int units = T * fs;
-    const int u0 = (int)((long long)units * warp / kWarps);
-    const int u1 = (int)((long long)units * (warp + 1) / kWarps);
-    unsigned sc[kStages][2 * MT], zr[kStages][2 * MT];
+    const int u0 = units * warp / kWarps;
+    const int u1 = units * (warp + 1) / kWarps;
+    unsigned sc[kStages][sRows][sGroups], zr[ZEROS ? kStages : 1][sRows][sGroups];
 
-    // the copies and scale loads of unit u into stage st
-    auto issue = [&](int u, int st) {
-      if (u < u1) {
-        const int t = u / fs, step = f0 + (u - t * fs);
-        const long long r0 = (long long)(t0 + t) * (16 * MT);
-        unsigned char* dst = ring + st * kStep;
+    // Where this warp's copies are: units left, tile and step, the lane's
+    // addresses in row g of the tile.
+    int cleft = u1 - u0, ct = fs > 0 ? u0 / fs : 0, cs = u0 - ct * fs;
+    const unsigned char *src = nullptr, *scp = nullptr, *zp = nullptr;
+    int rowsLeft = 0, bytesLeft = 0, groupsLeft = 0;
+    auto enter = [&]() {
+      const long long r0 = (long long)(t0 + ct) * kTileRows;
+      rowsLeft = (int)min((long long)a.rows - r0, (long long)kTileRows);
+      src = a.codes + (r0 + g) * a.ld_codes + ((long long)(f0 + cs) * kRow + c * 16);
+      bytesLeft = rowBytes - (f0 + cs) * kRow;
+      const int gi = (f0 + cs) * kGroups + sGroup0;
+      groupsLeft = groups - gi;
+      const long long r = r0 + g + 8 * sRow0;
+      scp = static_cast<const unsigned char*>(a.scales) + (r * a.ld_scales + gi) * scaleBytes;
+      if (ZEROS) zp = a.zeros + r * a.ld_zeros + gi;
+    };
+    enter();
+    if (f0 == s0) {
+      // Launched before the kernel ahead in the stream has ended: only the L2
+      // hears of the first codes until it has.
+      if (cleft > 0 && lane < rowsLeft)
+        prefetch_l2(a.codes + ((long long)(t0 + ct) * kTileRows + lane) * a.ld_codes +
+                    (long long)(f0 + cs) * kRow);
+      grid_dependency_wait();
+      grid_dependency_trigger();
+    }
+    auto issue = [&](int st) {
+      if (cleft > 0) {
         if (ALIGNED) {
-          const long long off = (long long)step * 64 + (lane & 3) * 16;
-          const int left = (int)min(rowBytes - off, 16LL);
+          if (rowsLeft == kTileRows && bytesLeft >= kRow) {
 #pragma unroll
-          for (int i = 0; i < 2 * MT; ++i) {
-            const int row = (lane >> 2) + 8 * i;
-            if (left > 0 && r0 + row < a.rows)
-              cp_async16_part(dst + row * 64 + chunk_at(row, lane & 3) * 16,
-                              a.codes + (r0 + row) * a.ld_codes + off, left);
+            for (int i = 0; i < kRows; ++i) {
+              const unsigned char* q = src + i * rows8;
+#pragma unroll
+              for (int j = 0; j < kRow / 64; ++j)
+                cp_async16(put[j] + st * kStep + 8 * i * kPitch, q + 64 * j);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+              const unsigned char* q = src + i * rows8;
+              const int left = g + 8 * i < rowsLeft ? bytesLeft - c * 16 : 0;
+#pragma unroll
+              for (int j = 0; j < kRow / 64; ++j)
+                if (left > 64 * j)
+                  cp_async16_part(put[j] + st * kStep + 8 * i * kPitch, q + 64 * j,
+                                  min(left - 64 * j, 16));
+            }
           }
         } else {
-          // 5 chunks of each row, from the aligned address at or below its start
-#pragma unroll
-          for (int i = 0; i < (5 * 16 * MT + 31) / 32; ++i) {
-            const int id = lane + 32 * i;
-            const int row = id / 5, j = id - row * 5;
-            if (row < 16 * MT && r0 + row < a.rows) {
-              const unsigned char* first = a.codes + (r0 + row) * a.ld_codes;
-              const unsigned char* src = reinterpret_cast<const unsigned char*>(
-                  (reinterpret_cast<uintptr_t>(first + (long long)step * 64) & ~(uintptr_t)15) +
-                  16 * j);
-              const unsigned char* end = first + rowBytes;
-              if (src < end) {
-                if (src >= a.codes && src + 16 <= p.codesEnd) {
-                  cp_async16_part(dst + row * 80 + j * 16, src, 16);
-                } else {  // the ends of the array: byte by byte
-                  for (int b = 0; b < 16; ++b)
-                    if (src + b >= a.codes && src + b < p.codesEnd)
-                      dst[row * 80 + j * 16 + b] = src[b];
-                }
+          // the aligned chunks of each row from its start rounded down
+          constexpr int kChunks = kPitch / 16;
+          const long long r0 = (long long)(t0 + ct) * kTileRows;
+          for (int id = lane; id < kChunks * rowsLeft; id += 32) {
+            const int row = id / kChunks, j = id - row * kChunks;
+            const unsigned char* first = a.codes + (r0 + row) * a.ld_codes;
+            const unsigned char* from =
+                reinterpret_cast<const unsigned char*>(
+                    reinterpret_cast<uintptr_t>(first + (long long)(f0 + cs) * kRow) &
+                    ~(uintptr_t)15) + 16 * j;
+            const unsigned to = ring + st * kStep + row * kPitch + j * 16;
+            if (from < first + rowBytes) {
+              if (from >= a.codes && from + 16 <= p.codesEnd) {
+                cp_async16(to, from);
+              } else {  // the ends of the array: byte by byte
+                for (int b = 0; b < 16; ++b)
+                  if (from + b >= a.codes && from + b < p.codesEnd) sts8(to + b, from[b]);
               }
             }
           }
         }
-        const int gi = step * kGroups + (kGroups == 4 ? c : kGroups == 2 ? c >> 1 : 0);
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-          const long long row = min(r0 + g + 8 * i, (long long)a.rows - 1);
-          sc[st][i] = gi < groups ? scale_raw(a.scales, a.scale_type, row * a.ld_scales + gi) : 0u;
-          zr[st][i] = a.zeros && gi < groups ? (unsigned)__ldg(a.zeros + row * a.ld_zeros + gi)
-                                             : 8u;
+        for (int i = 0; i < sRows; ++i)
+#pragma unroll
+          for (int l = 0; l < sGroups; ++l) {
+            sc[st][i][l] = 0u;
+            if (ZEROS) zr[st][i][l] = 8u;
+            if (g + 8 * (sRow0 + i) < rowsLeft && l < groupsLeft) {
+              const unsigned char* q = scp + i * scales8;
+              sc[st][i][l] = scaleBytes == 4
+                                 ? __ldg(reinterpret_cast<const unsigned*>(q) + l)
+                                 : (unsigned)__ldg(reinterpret_cast<const unsigned short*>(q) + l);
+              if (ZEROS) zr[st][i][l] = __ldg(zp + i * zeros8 + l);
+            }
+          }
+        --cleft;
+        if (++cs == fs) {
+          cs = 0;
+          ++ct;
+          enter();
+        } else {
+          src += kRow;
+          bytesLeft -= kRow;
+          scp += kGroups * scaleBytes;
+          groupsLeft -= kGroups;
+          if (ZEROS) zp += kGroups;
         }
       }
       cp_async_commit();
     };
 #pragma unroll
-    for (int st = 0; st < kStages - 1; ++st) issue(u0 + st, st);
+    for (int st = 0; st < kStages - 1; ++st) issue(st);
 
     // x of this phase, in fragment order: [step][word][column][c]
     if (f0 != s0) __syncthreads();  // the last phase's readers are done
-    for (int i = threadIdx.x; i < fs * 16 * p.n; i += kThreads) {
-      const int cc = i & 3, v = (i >> 2) % p.n, t = (i >> 2) / p.n;  // t: step * 4 + word
-      const int step = t >> 2, word = t & 3;
-      const long long k = (long long)(f0 + step) * 128 + (word / kWords) * G + cc * (G / 4) +
-                          (word % kWords) * 8;
-      stage_x<X>(x + v * p.ldx, k, a.cols, p.xVec, xs + ((size_t)t * NB + v * kParts) * 4 + cc, 4);
+    // (a piece: 8 entries of one vector; a thread fetches several at a time, of
+    // one vector or of the same columns of several)
+    {
+      constexpr int kBatch = kParts == 1 ? 4 : 2;
+      const int places = fs * kStepWords * 4;
+      auto entry = [&](int i) {  // the columns of place i: step, word and c
+        const int word = (i >> 2) % kStepWords;
+        return (long long)(f0 + (i >> 2) / kStepWords) * kStepCols + (word / kWords) * G +
+               (i & 3) * (G / 4) + (word % kWords) * 8;
+      };
+      Pack<X, 8> held[kBatch];
+      if (p.n == 1) {
+        for (int i0 = threadIdx.x; i0 < places; i0 += kBatch * kThreads) {
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q)
+            if (i0 + q * kThreads < places)
+              held[q] = fetch_x<X>(x, entry(i0 + q * kThreads), a.cols, p.xVec);
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q) {
+            const int i = i0 + q * kThreads;
+            if (i < places) stage_x<X>(held[q], xs + (i >> 2) * (kParts * 4) + (i & 3));
+          }
+        }
+      } else {
+        const int sets = (p.n + kBatch - 1) / kBatch;
+        for (int j = threadIdx.x; j < places * sets; j += kThreads) {
+          const int set = j / places, i = j - set * places, v0 = set * kBatch;
+          const long long k = entry(i);
+          const X* from = x + v0 * p.ldx;
+          uint4* to = xs + (i >> 2) * xWord4 + v0 * (kParts * 4) + (i & 3);
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q)
+            if (v0 + q < p.n) held[q] = fetch_x<X>(from + q * p.ldx, k, a.cols, p.xVec);
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q)
+            if (v0 + q < p.n) stage_x<X>(held[q], to + q * (kParts * 4));
+        }
+      }
     }
     __syncthreads();
 
-    float acc[MT][NT][4];
+    float acc[2][NT][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][nt][i] = 0.0f;
 
-    int tile = fs > 0 ? u0 / fs : 0, at = u0 - tile * fs;  // unit being consumed
-    for (int u = u0; u < u1; u += kStages) {
+    // The unit being consumed. A column that is not there is read as the last
+    // one: what an mma leaves in its place is never looked at.
+    int tile = fs > 0 ? u0 / fs : 0, at = u0 - tile * fs;
+    unsigned xl[NT];
+    const int xWord = xWord4 * 16;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      xl[nt] = xs0 + min(nt * 8 + g, NB - 1) * 64 + c * 16 + at * kStepWords * xWord;
+    for (int left = u1 - u0; left > 0;) {
 #pragma unroll
       for (int st = 0; st < kStages; ++st) {
-        if (u + st < u1) {
+        if (left > 0) {
           cp_async_wait<kStages - 2>();
           __syncwarp();
-          issue(u + st + kStages - 1, (st + kStages - 1) % kStages);
-          const unsigned char* buf = ring + st * kStep;
-          const uint4* xb = xs + (size_t)at * 16 * NB + c;
+          issue((st + kStages - 1) % kStages);
+          // this lane's scales and biases, to be passed among the four
+          float sv[sRows][sGroups];
+          unsigned zv[sRows][sGroups];
+#pragma unroll
+          for (int i = 0; i < sRows; ++i)
+#pragma unroll
+            for (int l = 0; l < sGroups; ++l) {
+              sv[i][l] = scale_value(sc[st][i][l], scaleShift, scaleHalf);
+              if (ZEROS) zv[i][l] = Op::kMagic + zr[ZEROS ? st : 0][i][l] * 0x00010001u;
+            }
+          unsigned shift[kRows];
+          if (!ALIGNED) {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+              const long long r = (long long)(t0 + tile) * kTileRows + g + 8 * i;
+              shift[i] = (unsigned)(reinterpret_cast<uintptr_t>(a.codes + r * a.ld_codes) & 15);
+            }
+          }
 #pragma unroll
           for (int gr = 0; gr < kGroups; ++gr) {
-            float part[MT][NT][4];
-            unsigned bias[2 * MT];
-            float s[2 * MT];
+            float s[kRows];
+            unsigned bias[kRows];
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) {
-              unsigned raw = sc[st][i], z = zr[st][i];
-              if (kGroups > 1) {
-                const int from = (lane & ~3) + gr * (4 / kGroups);
-                raw = __shfl_sync(kFullMask, raw, from);
-                z = __shfl_sync(kFullMask, z, from);
-              }
-              s[i] = scale_value(raw, a.scale_type);
-              bias[i] = Op::kMagic | z | z << 16;
+            for (int i = 0; i < kRows; ++i) {
+              const int from = (lane & ~3) + (kGroups == 1   ? i
+                                              : kGroups == 2 ? 2 * gr + (i >> 1)
+                                              : kGroups == 4 ? gr
+                                                             : gr >> 1);
+              const int row = kGroups == 1 ? 0 : kGroups == 2 ? i & 1 : i;
+              const int l = kGroups == 8 ? gr & 1 : 0;
+              s[i] = __shfl_sync(kFullMask, sv[row][l], from);
+              bias[i] = ZEROS ? __shfl_sync(kFullMask, zv[row][l], from) : Op::kMagic + 0x00080008u;
             }
+            unsigned w[kRows][kWords];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) part[m][nt][i] = 0.0f;
-            unsigned w[2 * MT][kWords];
-#pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) {
-              const int row = g + 8 * i;
+            for (int i = 0; i < kRows; ++i) {
               if (ALIGNED) {
-                const int byte = gr * (G / 2) + c * (G / 8);
-                const unsigned char* q =
-                    buf + row * 64 + chunk_at(row, byte >> 4) * 16 + (byte & 15);
+                const unsigned q = get[gr] + st * kStep + 8 * i * kPitch;
                 if (kWords == 4) {
-                  const uint4 v = *reinterpret_cast<const uint4*>(q);
+                  const uint4 v = lds128(q);
                   w[i][0] = v.x;
                   w[i][1 % kWords] = v.y;
                   w[i][2 % kWords] = v.z;
                   w[i][3 % kWords] = v.w;
                 } else if (kWords == 2) {
-                  const uint2 v = *reinterpret_cast<const uint2*>(q);
+                  const uint2 v = lds64(q);
                   w[i][0] = v.x;
                   w[i][1 % kWords] = v.y;
                 } else {
-                  w[i][0] = *reinterpret_cast<const unsigned*>(q);
+                  w[i][0] = lds32(q);
                 }
               } else {
-                const long long r = (long long)(t0 + tile) * (16 * MT) + row;
-                const unsigned shift =
-                    (unsigned)(reinterpret_cast<uintptr_t>(a.codes + r * a.ld_codes) & 15);
-                const unsigned byte = shift + gr * (G / 2) + c * (G / 8);
-                const unsigned* q = reinterpret_cast<const unsigned*>(buf + row * 80) + (byte >> 2);
-                unsigned lo = q[0];
+                const unsigned byte = shift[i] + gr * (G / 2) + c * (G / 8);
+                const unsigned q = ring + st * kStep + (g + 8 * i) * kPitch + (byte & ~3u);
+                unsigned lo = lds32(q);
 #pragma unroll
-                for (int i2 = 0; i2 < kWords; ++i2) {
+                for (int k = 0; k < kWords; ++k) {
                   // the last word's upper neighbour is only needed off a word boundary
-                  const unsigned hi = (byte & 3) || i2 + 1 < kWords ? q[i2 + 1] : 0u;
-                  w[i][i2] = __funnelshift_r(lo, hi, 8 * (byte & 3));
+                  const unsigned hi = (byte & 3) || k + 1 < kWords ? lds32(q + 4 * k + 4) : 0u;
+                  w[i][k] = __funnelshift_r(lo, hi, 8 * (byte & 3));
                   lo = hi;
                 }
               }
             }
+            float part[2][NT][4];
 #pragma unroll
-            for (int i2 = 0; i2 < kWords; ++i2) {
+            for (int k = 0; k < kWords; ++k) {
               uint4 b[NT];
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                b[nt] = make_uint4(0, 0, 0, 0);
-                const int col = nt * 8 + g;
-                if (col < NB) b[nt] = xb[((gr * kWords + i2) * NB + col) * 4];
+                b[nt] = lds128(xl[nt]);
+                xl[nt] += xWord;
               }
 #pragma unroll
-              for (int m = 0; m < MT; ++m) {
+              for (int m = 0; m < 2; ++m) {
                 unsigned lo[4], hi[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                  lo[j] = unpack<Op>(w[2 * m][i2], j, bias[2 * m]);
-                  hi[j] = unpack<Op>(w[2 * m + 1][i2], j, bias[2 * m + 1]);
+                  lo[j] = unpack<Op>(w[2 * m][k], j, mask, magic, bias[2 * m]);
+                  hi[j] = unpack<Op>(w[2 * m + 1][k], j, mask, magic, bias[2 * m + 1]);
                 }
-                const unsigned f0a[4] = {lo[0], hi[0], lo[1], hi[1]};
-                const unsigned f1a[4] = {lo[2], hi[2], lo[3], hi[3]};
+                const unsigned a0[4] = {lo[0], hi[0], lo[1], hi[1]};
+                const unsigned a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  mma16816(part[m][nt], f0a, b[nt].x, b[nt].y, typename Op::T{});
-                  mma16816(part[m][nt], f1a, b[nt].z, b[nt].w, typename Op::T{});
+                  float(&d)[4] = part[m][nt];
+                  if (k == 0)
+                    mma16816(d, a0, b[nt].x, b[nt].y, 0.0f, 0.0f, 0.0f, 0.0f, OpT{});
+                  else
+                    mma16816(d, a0, b[nt].x, b[nt].y, d[0], d[1], d[2], d[3], OpT{});
+                  mma16816(d, a1, b[nt].z, b[nt].w, d[0], d[1], d[2], d[3], OpT{});
                 }
               }
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                   acc[m][nt][i] = fmaf(s[2 * m + (i >> 1)], part[m][nt][i], acc[m][nt][i]);
           }
-          ++at;
-          if (at == fs || u + st + 1 == u1) {  // the tile's end, or this warp's
+          --left;
+          if (++at == fs || left == 0) {  // the tile's end, or this warp's
             float* slot = slots + (size_t)(tile + warp) * slotFloats;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const int col = nt * 8 + 2 * c + (i & 1);
-                  if (col < NB) slot[col * (16 * MT) + m * 16 + g + 8 * (i >> 1)] = acc[m][nt][i];
+                  if (col < NB) slot[col * kTileRows + m * 16 + g + 8 * (i >> 1)] = acc[m][nt][i];
                   acc[m][nt][i] = 0.0f;
                 }
             at = 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              xl[nt] = xs0 + min(nt * 8 + g, NB - 1) * 64 + c * 16;
             ++tile;
           }
         }
@@ -438,30 +610,40 @@ __global__ void __launch_bounds__(kThreads, 2) k_q4_run(const RunArgs p) {
     }
     cp_async_wait<0>();
     __syncthreads();
-    // join the warps' partial sums of each output, in the order of the columns
+    // Join the warps' partial sums of each output, in the order of the columns.
+    // What is not finished yet is kept where the first of them was, or with
+    // several phases in `sums`.
     const bool last = f0 + p.phaseSteps >= s1;
-    for (int o = threadIdx.x; o < outs; o += kThreads) {
-      const int row = o % (16 * MT), v = (o / (16 * MT)) % p.n, t = o / (16 * MT * p.n);
-      float sum = f0 == s0 ? 0.0f : sums[o];
-      if (fs > 0) {
-        // the warp that holds unit u: the last w with units * w / kWarps <= u
-        const int w0 = (int)((((long long)t * fs + 1) * kWarps - 1) / units);
-        const int w1 = (int)((((long long)(t + 1) * fs) * kWarps - 1) / units);
-        for (int w = w0; w <= w1; ++w) {
-          if ((long long)units * w / kWarps == (long long)units * (w + 1) / kWarps) continue;
+    for (int tv = warp; tv < T * p.n; tv += kWarps) {  // a tile and vector, its rows the lanes
+      const int t = p.n == 1 ? tv : tv / p.n, v = tv - t * p.n;
+      const int o = tv * kTileRows + lane;
+      float sum = phases && f0 > s0 ? sums[o] : 0.0f;
+      float* const in = slots + (size_t)t * slotFloats + v * kParts * kTileRows + lane;
+      const int w0 = fs > 0 ? owner(t * fs, units) : 0;
+      const int w1 = fs > 0 ? owner((t + 1) * fs - 1, units) : -1;
+      if (units >= kWarps) {
+#pragma unroll 4
+        for (int w = w0; w <= w1; ++w)
 #pragma unroll
-          for (int q = 0; q < kParts; ++q)
-            sum += slots[(size_t)(t + w) * slotFloats + (v * kParts + q) * (16 * MT) + row];
-        }
+          for (int q = 0; q < kParts; ++q) sum += in[(size_t)w * slotFloats + q * kTileRows];
+      } else {
+        for (int w = w0; w <= w1; ++w)
+          if (owner(units * w / kWarps, units) == w)  // not an idle one
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) sum += in[(size_t)w * slotFloats + q * kTileRows];
       }
-      if (last && p.P == 1) {
-        const long long r = (long long)(t0 + t) * (16 * MT) + row;
+      if (!last) {
+        sums[o] = sum;
+      } else if (p.P == 1) {
+        const long long r = (long long)(t0 + t) * kTileRows + lane;
         if (r < a.rows) {
           if (p.c) sum += load_y(p.c, p.yType, v * p.ldc + r);
           store_y(p.y, p.yType, v * p.ldy + r, sum);
         }
-      } else {
+      } else if (phases) {
         sums[o] = sum;
+      } else {
+        in[(size_t)w0 * slotFloats] = sum;
       }
     }
     if (!last) __syncthreads();
@@ -470,67 +652,88 @@ __global__ void __launch_bounds__(kThreads, 2) k_q4_run(const RunArgs p) {
     namespace cgr = cooperative_groups;
     cgr::cluster_group cl = cgr::this_cluster();
     cl.sync();
-    for (int o = threadIdx.x + kThreads * rank; o < outs; o += kThreads * p.P) {
-      const int row = o % (16 * MT), v = (o / (16 * MT)) % p.n, t = o / (16 * MT * p.n);
-      const long long r = (long long)(t0 + t) * (16 * MT) + row;
-      if (r >= a.rows) continue;
-      float sum = 0.0f;
-      for (int q = 0; q < p.P; ++q) sum += *cl.map_shared_rank(sums + o, q);
-      if (p.c) sum += load_y(p.c, p.yType, v * p.ldc + r);
-      store_y(p.y, p.yType, v * p.ldy + r, sum);
+    // blocks with one more step than the others put a tile's first warp elsewhere
+    for (int tv = rank * kWarps + warp; tv < T * p.n; tv += kWarps << p.logP) {
+      const int t = p.n == 1 ? tv : tv / p.n, v = tv - t * p.n;
+      const long long r = (long long)(t0 + t) * kTileRows + lane;
+      const int rest = (v * kParts) * kTileRows + lane;
+      const int more = p.stepShare + 1, less = p.stepShare;
+      float* const here = sums + tv * kTileRows + lane;
+      float* const atMore = slots + (size_t)(t + owner(t * more, T * more)) * slotFloats + rest;
+      float* const atLess = slots + (size_t)(t + owner(t * less, T * less)) * slotFloats + rest;
+      float parts[8];  // all on their way before the first is added
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        parts[q] = q < p.P ? *cl.map_shared_rank(phases              ? here
+                                                 : q < p.stepRest ? atMore
+                                                                  : atLess, q)
+                           : 0.0f;
+      float sum = parts[0];
+#pragma unroll
+      for (int q = 1; q < 8; ++q) sum += parts[q];
+      if (r < a.rows) {
+        if (p.c) sum += load_y(p.c, p.yType, v * p.ldc + r);
+        store_y(p.y, p.yType, v * p.ldy + r, sum);
+      }
     }
     cl.sync();  // the others may still be reading this block's sums
   }
 }
 
 // --- launch --------------------------------------------------------------------------
-template <class X, int G, int NT, int MT, bool ALIGNED>
+template <class X, int G, int NT, bool ALIGNED, bool ZEROS>
 cudaError_t launch_one(const RunArgs& args, cudaStream_t s) {
-  constexpr int kRowBytes = ALIGNED ? 64 : 80;
-  const Plan plan = make_plan(args, 16 * MT, OpOf<X>::kParts * args.n,
-                              kWarps * kStages * 16 * MT * kRowBytes);
+  constexpr int kPitch = kStepColsOf<NT> / 2 + (ALIGNED ? 0 : 16);
+  auto kernel = k_q4_run<X, G, NT, ALIGNED, ZEROS>;
+  static Residency room;  // one per kernel
+  cudaError_t e = room.ask(reinterpret_cast<const void*>(kernel));
+  if (e != cudaSuccess) return e;
+  const Plan plan = make_plan(args, OpOf<X>::kParts * args.n, kStepColsOf<NT>,
+                              kWarps * kStagesOf<NT> * kTileRows * kPitch, room);
   RunArgs p = args;
   p.P = plan.P;
+  p.logP = plan.logP;
   p.phaseSteps = plan.phaseSteps;
   p.maxTiles = plan.maxTiles;
-  p.tiles = plan.tiles;
-  p.steps = plan.steps;
-  auto kernel = k_q4_run<X, G, NT, MT, ALIGNED>;
-  static SmemOnce once;  // one per kernel
-  cudaError_t e = once.allow(reinterpret_cast<const void*>(kernel));
-  if (e != cudaSuccess) return e;
+  p.tileShare = (int)(plan.tiles / plan.clusters);
+  p.tileRest = (int)(plan.tiles % plan.clusters);
+  p.stepShare = plan.steps / plan.P;
+  p.stepRest = plan.steps % plan.P;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(plan.clusters * plan.P));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = plan.smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = plan.P;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = plan.P;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = plan.P > 1 ? 1 : 0;
+  cfg.numAttrs = plan.P > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kernel, (const RunArgs)p);
   note_launches(1);
   return e;
 }
 
-template <class X, int G, bool ALIGNED>
-cudaError_t launch_tiles(const RunArgs& p, cudaStream_t s) {
-  return OpOf<X>::kParts * p.n <= 8 ? launch_one<X, G, 1, 1, ALIGNED>(p, s)
-                                    : launch_one<X, G, 2, 2, ALIGNED>(p, s);
+template <class X, int G, bool ZEROS>
+cudaError_t launch_group(const RunArgs& p, cudaStream_t s) {
+  const bool aligned = aligned16(p.a.codes) && (p.a.ld_codes % 16 == 0 || p.a.rows <= 1);
+  if (!aligned) return launch_one<X, G, 2, false, ZEROS>(p, s);
+  return OpOf<X>::kParts * p.n <= 8 ? launch_one<X, G, 1, true, ZEROS>(p, s)
+                                    : launch_one<X, G, 2, true, ZEROS>(p, s);
 }
 
 // Up to vectors_per_pass<X>() vectors in one launch.
 template <class X>
 cudaError_t launch_run(const RunArgs& p, cudaStream_t s) {
-  const bool aligned = aligned16(p.a.codes) && (p.a.ld_codes % 16 == 0 || p.a.rows <= 1);
+  const bool z = p.a.zeros != nullptr;
   switch (p.a.group) {
-    case 32: return aligned ? launch_tiles<X, 32, true>(p, s) : launch_tiles<X, 32, false>(p, s);
-    case 64: return aligned ? launch_tiles<X, 64, true>(p, s) : launch_tiles<X, 64, false>(p, s);
-    default:
-      return aligned ? launch_tiles<X, 128, true>(p, s) : launch_tiles<X, 128, false>(p, s);
+    case 32: return z ? launch_group<X, 32, true>(p, s) : launch_group<X, 32, false>(p, s);
+    case 64: return z ? launch_group<X, 64, true>(p, s) : launch_group<X, 64, false>(p, s);
+    default: return z ? launch_group<X, 128, true>(p, s) : launch_group<X, 128, false>(p, s);
   }
 }
 
