@@ -278,6 +278,18 @@ def spmv_run_csr_noalloc(num_rows, num_cols, nnz, row_ptrs, col_idx, value, x, y
 
 
 # --- dense tables: 4-bit matrices and token lookups --------------------------------
+# The handle of a device's current stream. torch.cuda.current_stream builds an
+# object for it, 2.8 us of a call that takes the GPU 4.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, t):
+    """The given stream, or the current one of tensor ``t``'s device."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _stream(stream)
+
+
 def _dtype(t, what):
     try:
         return DTYPES[t.dtype]
@@ -293,14 +305,14 @@ def _matrix(t, what, dtype=None):
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
     shape = t.shape
-    if len(shape) == 1:
-        rows, cols = 1, shape[0]
-        ld = cols
-        inner = t.stride(0)
-    elif len(shape) == 2:
+    if len(shape) == 2:
         rows, cols = shape
-        outer, inner = t.stride()
-        ld = outer if rows > 1 else cols
+        ld, inner = t.stride()
+        if rows <= 1:
+            ld = cols
+    elif len(shape) == 1:
+        rows, cols = 1, shape[0]
+        ld, inner = cols, t.stride(0)
     else:
         raise ValueError(f"{what}: expected one or two dimensions, got {len(shape)}")
     if inner != 1 and cols > 1:
@@ -350,7 +362,7 @@ def spmv_q4_quantize(w, codes, scales, group, zeros=None, back=None, stream=None
         bp, brows, bcols, ldb = _matrix(back, "back", w.dtype)
         if (brows, bcols) != (rows, cols):
             raise ValueError("back: expected the shape of w")
-    _check(_lib.spmv_q4_quantize(C.byref(a), _dtype(w, "w"), wp, ldw, bp, ldb, _stream(stream)),
+    _check(_lib.spmv_q4_quantize(C.byref(a), _dtype(w, "w"), wp, ldw, bp, ldb, _stream_of(stream, w)),
            "spmv_q4_quantize")
 
 
@@ -368,14 +380,7 @@ def spmv_q4_run(codes, scales, group, x, y, c=None, zeros=None, stream=None):
         if (cn, crows) != (n, rows):
             raise ValueError("c: expected the shape of y")
     _check(_lib.spmv_q4_run(C.byref(a), n, _dtype(x, "x"), xp, ldx, cp, ldc, _dtype(y, "y"), yp,
-                            ldy, _stream(stream)), "spmv_q4_run")
-
-
-def _lookup_out(out, n):
-    op, rows, dim, ldo = _matrix(out, "out")
-    if rows != n:
-        raise ValueError(f"out has {rows} rows for {n} tokens")
-    return op, dim, ldo
+                            ldy, _stream_of(stream, x)), "spmv_q4_run")
 
 
 def spmv_embed(table, tokens, out, scale=1.0, stream=None):
@@ -383,23 +388,22 @@ def spmv_embed(table, tokens, out, scale=1.0, stream=None):
     outside 0 .. vocab-1 gives a row of zeros."""
     tp, vocab, dim, ldt = _matrix(table, "table")
     kp, n, size = _tokens(tokens)
-    op, odim, ldo = _lookup_out(out, n)
-    if odim != dim:
-        raise ValueError(f"out has {odim} columns, the table {dim}")
+    op, rows, odim, ldo = _matrix(out, "out")
+    if rows != n or odim != dim:
+        raise ValueError(f"out {tuple(out.shape)} does not fit {n} tokens of {dim} columns")
     _check(_lib.spmv_embed(vocab, dim, _dtype(table, "table"), tp, ldt, n, size, kp, scale,
-                           _dtype(out, "out"), op, ldo, _stream(stream)), "spmv_embed")
+                           _dtype(out, "out"), op, ldo, _stream_of(stream, out)), "spmv_embed")
 
 
 def spmv_embed_q4(codes, scales, group, tokens, out, scale=1.0, zeros=None, stream=None):
     """As spmv_embed from a 4-bit table; ``tokens`` None: rows 0 .. len(out)-1."""
-    kp, n, size = _tokens(tokens) if tokens is not None else (None, None, 4)
-    op, dim, ldo = _lookup_out(out, n if n is not None else
-                               (out.shape[0] if out.dim() == 2 else 1))
+    op, rows, dim, ldo = _matrix(out, "out")
+    kp, n, size = _tokens(tokens) if tokens is not None else (None, rows, 4)
+    if rows != n:
+        raise ValueError(f"out has {rows} rows for {n} tokens")
     a = _q4_view(codes, scales, group, dim, zeros)
-    if n is None:
-        n = out.shape[0] if out.dim() == 2 else 1
     _check(_lib.spmv_embed_q4(C.byref(a), n, size, kp, scale, _dtype(out, "out"), op, ldo,
-                              _stream(stream)), "spmv_embed_q4")
+                              _stream_of(stream, out)), "spmv_embed_q4")
 
 
 def spmv_embed_grad_workspace(vocab, dim, n_tokens):
@@ -421,15 +425,15 @@ def spmv_embed_grad(g, tokens, dtable, scale=1.0, accumulate=False, workspace=No
     if count != n or ddim != dim:
         raise ValueError(f"g {tuple(g.shape)}, {count} tokens and dtable "
                          f"{tuple(dtable.shape)} do not fit")
-    st = _stream(stream)
+    st = _stream_of(stream, dtable)
     if workspace is None:
         nbytes = spmv_embed_grad_workspace(vocab, dim, n)
         # taken on the launching stream, so that torch reuses it only after the call's work
-        if st == torch.cuda.current_stream().cuda_stream:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        if stream is None or st == _stream_of(None, dtable):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dtable.device)
         else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(st)):
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+            with torch.cuda.stream(torch.cuda.ExternalStream(st, dtable.device)):
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dtable.device)
     _check(_lib.spmv_embed_grad(vocab, dim, _dtype(g, "g"), gp, ldg, n, size, kp, scale,
                                 1 if accumulate else 0, _dtype(dtable, "dtable"), dp, ldd,
                                 _ptr(workspace), workspace.numel() * workspace.element_size(),

@@ -58,6 +58,26 @@ inline bool misaligned(const void* p, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) != 0;
 }
 
+// Launches a kernel that may start before the one ahead of it in the stream has
+// ended (it waits for that by itself, grid_dependency_wait, before it touches
+// memory), which hides most of the gap between two short kernels.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s,
+                             A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  note_launches(1);
+  return e;
+}
+
 // E consecutive elements as one aligned access of E * sizeof(T) bytes (a
 // power of two, at most 32: two 16-byte accesses).
 template <class T, int E>

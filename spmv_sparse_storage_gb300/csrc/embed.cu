@@ -17,18 +17,39 @@ __device__ __forceinline__ long long token_at(const void* tokens, int wide, long
 }
 
 // ---------------------------------------------------------------------------
-// Lookup: one block per token.
+// Lookup: E elements to a lane and load, kRowLoads of them in flight, G lanes to
+// a token and stretch of its row. Bound by the bytes read and written.
 // ---------------------------------------------------------------------------
-template <class T, class O>
-__global__ void __launch_bounds__(256) k_embed(int vocab, int dim, const T* __restrict__ table,
-                                               long long ldt, const void* __restrict__ tokens,
-                                               int wide, float scale, O* __restrict__ out,
-                                               long long ldo) {
-  const long long t = blockIdx.x;
+constexpr int kRowLoads = 4;
+template <class T, class O, int E>
+__global__ void __launch_bounds__(256) k_embed(int n, int vocab, int dim, int logG,
+                                               const T* __restrict__ table, long long ldt,
+                                               const void* __restrict__ tokens, int wide,
+                                               float scale, O* __restrict__ out, long long ldo) {
+  grid_dependency_wait();
+  grid_dependency_trigger();
+  const int G = 1 << logG;
+  const long long t = (long long)blockIdx.x * (256 >> logG) + (threadIdx.x >> logG);
+  if (t >= n) return;
   const long long token = token_at(tokens, wide, t);
   const bool valid = token >= 0 && token < vocab;
-  for (int k = threadIdx.x; k < dim; k += blockDim.x)
-    out[t * ldo + k] = from_f32<O>(valid ? scale * to_f32(table[token * ldt + k]) : 0.0f);
+  const int k0 = ((int)blockIdx.y * kRowLoads * G + (threadIdx.x & (G - 1))) * E;
+  Pack<T, E> v[kRowLoads];
+#pragma unroll
+  for (int i = 0; i < kRowLoads; ++i) {
+    const int k = k0 + i * G * E;
+    if (valid && k < dim) v[i] = *reinterpret_cast<const Pack<T, E>*>(table + token * ldt + k);
+  }
+#pragma unroll
+  for (int i = 0; i < kRowLoads; ++i) {
+    const int k = k0 + i * G * E;
+    if (k >= dim) break;
+    Pack<O, E> o;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      o.v[e] = from_f32<O>(valid ? scale * to_f32(v[i].v[e]) : 0.0f);
+    *reinterpret_cast<Pack<O, E>*>(out + t * ldo + k) = o;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -200,15 +221,25 @@ int spmv_embed(int32_t vocab, int32_t dim, spmv_dtype tableType, const void* d_t
   int st = check_current_device_ptrs(ptrs, 3);
   if (st != SPMV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int tb = dtype_bytes(tableType), ob = dtype_bytes(outType);
+  const bool wide = dim % 8 == 0 && aligned16(d_table) && ld_table * tb % 16 == 0 &&
+                    aligned16(d_out) && ld_out * ob % 16 == 0;
+  const int E = wide ? 8 : 1;
+  const long long pieces = ((long long)dim + E - 1) / E;
+  int logG = 0;
+  while (logG < 5 && (kRowLoads << logG) < pieces) ++logG;
+  const long long y = (pieces + (kRowLoads << logG) - 1) / (kRowLoads << logG);
+  if (y > 65535) return SPMV_ERR_TOO_LARGE;
+  const dim3 grid((unsigned)(((long long)nTokens + (256 >> logG) - 1) / (256 >> logG)), (unsigned)y);
   return record_cuda(with_dtype(tableType, [&](auto tv) {
     return with_dtype(outType, [&](auto ov) {
       using T = decltype(tv);
       using O = decltype(ov);
-      k_embed<T, O><<<(unsigned)nTokens, 256, 0, s>>>(
-          vocab, dim, static_cast<const T*>(d_table), ld_table, d_tokens, indexBytes == 8, scale,
-          static_cast<O*>(d_out), ld_out);
-      note_launches(1);
-      return cudaGetLastError();
+      return launch_dependent(wide ? k_embed<T, O, 8> : k_embed<T, O, 1>, grid, 256, s,
+                              (int)nTokens, (int)vocab, (int)dim, logG,
+                              static_cast<const T*>(d_table), (long long)ld_table, d_tokens,
+                              (int)(indexBytes == 8), scale, static_cast<O*>(d_out),
+                              (long long)ld_out);
     });
   }));
 }

@@ -18,11 +18,193 @@ __device__ __forceinline__ float scale_at(const void* scales, int type, long lon
 }
 
 // ---------------------------------------------------------------------------
-// Conversion: one warp per row and group.
+// Conversion. Of a group: the least and the largest weight, the scale, and per
+// weight the code round(w / scale) + zero. Bound by the bytes of W, of the codes
+// and of the values where they are asked for, as long as the arithmetic per
+// weight stays short: with both the time of its bytes leaves 24 instructions.
 // ---------------------------------------------------------------------------
+constexpr float kMaxFinite = 3.402823466e38f;
+constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
+
+struct GroupCodes {
+  float step, inv, low, high;  // code - zero is in [low, high]
+  unsigned zero;
+  bool usable, plain;          // plain: quotients by inv, and never below low
+};
+// The least normal number of a scale's type: below it a scale is so coarse that
+// quotients leave the codes' range, and 1 / scale may overflow.
+template <class S>
+constexpr float kLeastNormal = 1.2e-37f;
+template <>
+constexpr float kLeastNormal<__half> = 6.2e-5f;
+__device__ __forceinline__ float reciprocal(float v) {  // to 1 unit in the last place
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// w / step from inv = 1 / step (1 + 2^-23): the product's error is taken out by
+// the residual w - t step, which fma gives exactly (a Newton correction). What is
+// left is 2^-45 of the quotient before the last rounding, so that a half integer,
+// which 16-bit weights and scales hit now and then, comes out as one.
+__device__ __forceinline__ float quotient(float w, float step, float inv) {
+  const float t = w * inv;
+  return fmaf(fmaf(-t, step, w), inv, t);
+}
+// lo <= 0 <= hi: the range of a group's weights (a NaN if one of them is).
+template <class S>
+__device__ __forceinline__ GroupCodes group_codes(float lo, float hi, bool zeros, S* scale) {
+  float raw = zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f;
+  if (!(hi <= kMaxFinite && lo >= -kMaxFinite)) raw = __int_as_float(0x7fc00000);
+  *scale = from_f32<S>(raw);
+  GroupCodes c;
+  c.step = to_f32(*scale);
+  c.usable = c.step > 0.0f && c.step <= kMaxFinite;
+  c.plain = c.usable && c.step >= kLeastNormal<S>;
+  c.inv = reciprocal(c.step);
+  float zero = 8.0f;
+  if (zeros) {
+    const float z = c.plain ? quotient(-lo, c.step, c.inv) : -lo / c.step;
+    zero = c.usable ? fminf(fmaxf(rintf(z), 0.0f), 15.0f) : 0.0f;
+  }
+  c.zero = (unsigned)zero;
+  c.low = -zero;
+  c.high = 15.0f - zero;
+  return c;
+}
+// code - zero + kRound for N weights.
+template <int N>
+__device__ __forceinline__ void rounded_codes(const float (&w)[N], const GroupCodes& c,
+                                              float (&u)[N]) {
+  if (c.plain) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) u[e] = fminf(quotient(w[e], c.step, c.inv), c.high) + kRound;
+  } else {
+    for (int e = 0; e < N; ++e)
+      u[e] = c.usable ? fminf(fmaxf(w[e] / c.step, c.low), c.high) + kRound : kRound;
+  }
+}
+
+// The range of the 16 weights of each of the LANES lanes that share a group, in
+// pairs for the 16-bit types; NaN wins. hi = max(0, w), lo = min(0, w).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+template <int LANES>
+__device__ __forceinline__ void group_range(const Pack<float, 8> (&v)[2], float& lo, float& hi) {
+  float up = 0.0f, down = 0.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      up = max_nan(up, v[h].v[e]);
+      down = max_nan(down, -v[h].v[e]);
+    }
+#pragma unroll
+  for (int off = 1; off < LANES; off *= 2) {
+    up = max_nan(up, __shfl_xor_sync(kFullMask, up, off));
+    down = max_nan(down, __shfl_xor_sync(kFullMask, down, off));
+  }
+  hi = up;
+  lo = -down;
+}
+template <int LANES, class P, class W>
+__device__ __forceinline__ void pair_range(const Pack<W, 8> (&v)[2], float& lo, float& hi) {
+  const P* p = reinterpret_cast<const P*>(&v);
+  P up = p[0], down = p[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) {
+    up = __hmax2_nan(up, p[e]);
+    down = __hmin2_nan(down, p[e]);
+  }
+  down = __hneg2(down);
+  P both;  // (largest, - least)
+  both.x = __hmax_nan(up.x, up.y);
+  both.y = __hmax_nan(down.x, down.y);
+#pragma unroll
+  for (int off = 1; off < LANES; off *= 2)
+    both = __hmax2_nan(both, __shfl_xor_sync(kFullMask, both, off));
+  hi = max_nan(to_f32(both.x), 0.0f);
+  lo = -max_nan(to_f32(both.y), 0.0f);
+}
+template <int LANES>
+__device__ __forceinline__ void group_range(const Pack<__half, 8> (&v)[2], float& lo, float& hi) {
+  pair_range<LANES, __half2>(v, lo, hi);
+}
+template <int LANES>
+__device__ __forceinline__ void group_range(const Pack<__nv_bfloat16, 8> (&v)[2], float& lo,
+                                            float& hi) {
+  pair_range<LANES, __nv_bfloat162>(v, lo, hi);
+}
+
+// Rows of whole 8-weight pieces on 16-byte boundaries: a lane holds 16
+// consecutive weights, a warp 512 of a row, kPieces such stretches in flight; a
+// group is G / 16 neighbouring lanes, and 8 codes of a lane are one word.
+constexpr int kPieces = 2;
+template <class W, class S, int G>
+__global__ void __launch_bounds__(256) k_q4_quantize_wide(spmv_q4 a, const W* w, long long ldw,
+                                                          W* back, long long ldb,
+                                                          unsigned sets) {
+  constexpr int LANES = G / 16;
+  grid_dependency_wait();
+  grid_dependency_trigger();
+  const int lane = threadIdx.x & 31;
+  const unsigned rows8 = blockIdx.x / sets, set = blockIdx.x - rows8 * sets;
+  const long long row = (long long)rows8 * 8 + threadIdx.x / 32;
+  if (row >= a.rows) return;
+  const int col0 = (int)set * (512 * kPieces) + lane * 16;
+  Pack<W, 8> v[kPieces][2];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = col0 + 512 * i + 8 * h;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][h].v[e] = from_f32<W>(0.0f);
+      if (col < a.cols) v[i][h] = *reinterpret_cast<const Pack<W, 8>*>(w + row * ldw + col);
+    }
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    float lo, hi;
+    group_range<LANES>(v[i], lo, hi);
+    S scale;
+    const GroupCodes c = group_codes<S>(lo, hi, a.zeros != nullptr, &scale);
+    const int col = col0 + 512 * i;
+    if (col >= a.cols) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (col + 8 * h >= a.cols) break;
+      float in[8], u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) in[e] = to_f32(v[i][h].v[e]);
+      rounded_codes<8>(in, c, u);
+      // code - zero sits in the low bits of u, so the word of codes is the sum
+      // of those bits, shifted, and a constant
+      unsigned word = (c.zero - 0x4b400000u) * 0x11111111u;
+      Pack<W, 8> o;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        word += __float_as_uint(u[e]) << (4 * e);
+        o.v[e] = from_f32<W>((u[e] - kRound) * c.step);
+      }
+      *reinterpret_cast<unsigned*>(a.codes + row * a.ld_codes + (col + 8 * h) / 2) = word;
+      if (back) *reinterpret_cast<Pack<W, 8>*>(back + row * ldb + col + 8 * h) = o;
+    }
+    if (lane % LANES == 0) {
+      const int gi = col / G;
+      static_cast<S*>(a.scales)[row * a.ld_scales + gi] = scale;
+      if (a.zeros) a.zeros[row * a.ld_zeros + gi] = (uint8_t)c.zero;
+    }
+  }
+}
+
+// Any rows: one warp per row and group, two weights of a byte to a lane.
 template <class W, class S>
 __global__ void __launch_bounds__(256) k_q4_quantize(spmv_q4 a, const W* w, long long ldw,
                                                      W* back, long long ldb) {
+  grid_dependency_wait();
+  grid_dependency_trigger();
   const int groups = (a.cols + a.group - 1) / a.group;
   const long long id = (long long)blockIdx.x * 8 + threadIdx.x / 32;
   const int lane = threadIdx.x & 31;
@@ -31,71 +213,87 @@ __global__ void __launch_bounds__(256) k_q4_quantize(spmv_q4 a, const W* w, long
   const int gi = (int)(id % groups);
   const int k0 = gi * a.group, k1 = min(k0 + a.group, a.cols);
   float v[4];
-  float lo = 0.0f, hi = 0.0f, bad = 0.0f;
+  float up = 0.0f, down = 0.0f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int k = k0 + 2 * lane + (j & 1) + 64 * (j >> 1);
     v[j] = k < k1 ? to_f32(w[r * ldw + k]) : 0.0f;
-    lo = fminf(lo, v[j]);
-    hi = fmaxf(hi, v[j]);
-    if (!(fabsf(v[j]) <= 3.402823466e38f)) bad = 1.0f;
+    up = max_nan(up, v[j]);
+    down = max_nan(down, -v[j]);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(kFullMask, lo, off));
-    hi = fmaxf(hi, __shfl_xor_sync(kFullMask, hi, off));
-    bad = fmaxf(bad, __shfl_xor_sync(kFullMask, bad, off));
+    up = max_nan(up, __shfl_xor_sync(kFullMask, up, off));
+    down = max_nan(down, __shfl_xor_sync(kFullMask, down, off));
   }
-  float raw = a.zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f;
-  if (bad != 0.0f) raw = __int_as_float(0x7fc00000);
-  const S held = from_f32<S>(raw);
-  const float step = to_f32(held);
-  const bool usable = step > 0.0f && step <= 3.402823466e38f;
-  float zero = 8.0f;
-  if (a.zeros) zero = usable ? fminf(fmaxf(rintf(-lo / step), 0.0f), 15.0f) : 0.0f;
+  S scale;
+  const GroupCodes c = group_codes<S>(-down, up, a.zeros != nullptr, &scale);
   if (lane == 0) {
-    static_cast<S*>(a.scales)[r * a.ld_scales + gi] = held;
-    if (a.zeros) a.zeros[r * a.ld_zeros + gi] = (uint8_t)zero;
+    static_cast<S*>(a.scales)[r * a.ld_scales + gi] = scale;
+    if (a.zeros) a.zeros[r * a.ld_zeros + gi] = (uint8_t)c.zero;
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int k = k0 + 2 * lane + 64 * j;
     if (k >= k1) continue;
-    float q[2];
+    const float in[2] = {v[2 * j], v[2 * j + 1]};
+    float u[2];
+    rounded_codes<2>(in, c, u);
+    unsigned q[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      q[i] = usable ? fminf(fmaxf(rintf(v[2 * j + i] / step) + zero, 0.0f), 15.0f) : zero;
-      if (k + i >= k1)
-        q[i] = 0.0f;
-      else if (back)
-        back[r * ldb + k + i] = from_f32<W>((q[i] - zero) * step);
+      const float d = u[i] - kRound;
+      q[i] = k + i < k1 ? (unsigned)((int)d + (int)c.zero) : 0u;
+      if (back && k + i < k1) back[r * ldb + k + i] = from_f32<W>(d * c.step);
     }
-    a.codes[r * a.ld_codes + k / 2] = (uint8_t)((int)q[0] | (int)q[1] << 4);
+    a.codes[r * a.ld_codes + k / 2] = (uint8_t)(q[0] | q[1] << 4);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Rows back in dense form: one block per token.
+// Rows back in dense form: E columns to a lane and load, kRowLoads of them in
+// flight, G lanes to a token and stretch. Bound by the bytes written.
 // ---------------------------------------------------------------------------
-template <class O>
-__global__ void __launch_bounds__(256) k_embed_q4(spmv_q4 a, const void* __restrict__ tokens,
-                                                  int wide, float scale, O* __restrict__ out,
+constexpr int kRowLoads = 4;
+template <class O, int E>
+__global__ void __launch_bounds__(256) k_embed_q4(spmv_q4 a, int n, int logG, int logGroup,
+                                                  const void* __restrict__ tokens, int wide,
+                                                  float scale, O* __restrict__ out,
                                                   long long ldo) {
-  const long long t = blockIdx.x;
+  grid_dependency_wait();
+  grid_dependency_trigger();
+  const int G = 1 << logG;
+  const long long t = (long long)blockIdx.x * (256 >> logG) + (threadIdx.x >> logG);
+  if (t >= n) return;
   const long long r = !tokens ? t
                       : wide  ? static_cast<const long long*>(tokens)[t]
                               : (long long)static_cast<const int*>(tokens)[t];
   const bool valid = r >= 0 && r < a.rows;
-  for (int k = threadIdx.x; k < a.cols; k += blockDim.x) {
-    float v = 0.0f;
-    if (valid) {
-      const int gi = k / a.group;
-      const int b = a.codes[r * a.ld_codes + k / 2];
-      const float zero = a.zeros ? (float)a.zeros[r * a.ld_zeros + gi] : 8.0f;
-      v = ((float)((k & 1) ? b >> 4 : b & 15) - zero) *
-          scale_at(a.scales, a.scale_type, r * a.ld_scales + gi) * scale;
+  const int k0 = ((int)blockIdx.y * kRowLoads * G + (threadIdx.x & (G - 1))) * E;
+  unsigned w[kRowLoads];
+  float s[kRowLoads], z[kRowLoads];
+#pragma unroll
+  for (int i = 0; i < kRowLoads; ++i) {
+    const int k = k0 + i * G * E;
+    w[i] = 0;
+    s[i] = 0.0f;
+    z[i] = 8.0f;
+    if (valid && k < a.cols) {
+      const uint8_t* q = a.codes + r * a.ld_codes + k / 2;
+      w[i] = E == 8 ? *reinterpret_cast<const unsigned*>(q) : (unsigned)*q >> (4 * (k & 1));
+      s[i] = scale_at(a.scales, a.scale_type, r * a.ld_scales + (k >> logGroup));
+      if (a.zeros) z[i] = (float)a.zeros[r * a.ld_zeros + (k >> logGroup)];
     }
-    out[t * ldo + k] = from_f32<O>(v);
+  }
+#pragma unroll
+  for (int i = 0; i < kRowLoads; ++i) {
+    const int k = k0 + i * G * E;
+    if (k >= a.cols) break;
+    Pack<O, E> o;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      o.v[e] = from_f32<O>(valid ? ((float)((w[i] >> (4 * e)) & 15u) - z[i]) * s[i] * scale : 0.0f);
+    *reinterpret_cast<Pack<O, E>*>(out + t * ldo + k) = o;
   }
 }
 
@@ -249,16 +447,27 @@ int spmv_q4_quantize(const spmv_q4* a, spmv_dtype wType, const void* d_w, int64_
   st = check_current_device_ptrs(arr, 5);
   if (st != SPMV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const long long warps = a->rows * groups;
-  if ((warps + 7) / 8 > 0x7fffffffLL) return SPMV_ERR_TOO_LARGE;
+  const bool wide = a->cols % 8 == 0 && aligned16(d_w) && ldw * wb % 16 == 0 &&
+                    aligned16(d_back) && (!d_back || ld_back * wb % 16 == 0) &&
+                    !misaligned(a->codes, 4) && a->ld_codes % 4 == 0;
+  const long long sets = ((long long)a->cols + 512 * kPieces - 1) / (512 * kPieces);
+  const long long blocks =
+      wide ? ((long long)a->rows + 7) / 8 * sets : (a->rows * groups + 7) / 8;
+  if (blocks > 0x7fffffffLL) return SPMV_ERR_TOO_LARGE;
   return record_cuda(with_dtype(wType, [&](auto wv) {
     return with_dtype(a->scale_type, [&](auto sv) {
       using W = decltype(wv);
       using S = decltype(sv);
-      k_q4_quantize<W, S><<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(
-          *a, static_cast<const W*>(d_w), ldw, static_cast<W*>(d_back), ld_back);
-      note_launches(1);
-      return cudaGetLastError();
+      const W* src = static_cast<const W*>(d_w);
+      W* back = static_cast<W*>(d_back);
+      if (!wide)
+        return launch_dependent(k_q4_quantize<W, S>, dim3((unsigned)blocks), 256, s, *a, src,
+                                (long long)ldw, back, (long long)ld_back);
+      auto kernel = a->group == 32   ? k_q4_quantize_wide<W, S, 32>
+                    : a->group == 64 ? k_q4_quantize_wide<W, S, 64>
+                                     : k_q4_quantize_wide<W, S, 128>;
+      return launch_dependent(kernel, dim3((unsigned)blocks), 256, s, *a, src, (long long)ldw,
+                              back, (long long)ld_back, (unsigned)sets);
     });
   }));
 }
@@ -341,12 +550,21 @@ int spmv_embed_q4(const spmv_q4* a, int32_t nTokens, int32_t indexBytes, const v
   st = check_current_device_ptrs(ptrs, 5);
   if (st != SPMV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool wide = a->cols % 8 == 0 && aligned16(d_out) && ld_out * ob % 16 == 0 &&
+                    !misaligned(a->codes, 4) && a->ld_codes % 4 == 0;
+  const int E = wide ? 8 : 1;
+  const long long pieces = ((long long)a->cols + E - 1) / E;
+  int logG = 0;
+  while (logG < 5 && (kRowLoads << logG) < pieces) ++logG;
+  const long long y = (pieces + (kRowLoads << logG) - 1) / (kRowLoads << logG);
+  if (y > 65535) return SPMV_ERR_TOO_LARGE;
+  const dim3 grid((unsigned)(((long long)nTokens + (256 >> logG) - 1) / (256 >> logG)), (unsigned)y);
+  const int logGroup = a->group == 32 ? 5 : a->group == 64 ? 6 : 7;
   return record_cuda(with_dtype(outType, [&](auto ov) {
     using O = decltype(ov);
-    k_embed_q4<O><<<(unsigned)nTokens, 256, 0, s>>>(*a, d_tokens, indexBytes == 8, scale,
-                                                    static_cast<O*>(d_out), ld_out);
-    note_launches(1);
-    return cudaGetLastError();
+    return launch_dependent(wide ? k_embed_q4<O, 8> : k_embed_q4<O, 1>, grid, 256, s, *a,
+                            (int)nTokens, logG, logGroup, d_tokens, (int)(indexBytes == 8), scale,
+                            static_cast<O*>(d_out), (long long)ld_out);
   }));
 }
 
