@@ -4,6 +4,10 @@
 // (scale) per row, at the token's column, and the table; its gradient with
 // respect to the table is the transposed product: row v of the gradient is
 // scale times the sum of the rows of g whose token is v.
+#include <cooperative_groups.h>
+
+#include <atomic>
+
 #include "dtypes.cuh"
 #include "device_util.cuh"
 #include "internal.h"
@@ -53,77 +57,276 @@ __global__ void __launch_bounds__(256) k_embed(int n, int vocab, int dim, int lo
 }
 
 // ---------------------------------------------------------------------------
-// Gradient. The tokens are sorted (equal ones in order); the sorted positions
-// are cut into chunks of kSumChunk, each summed by one group of threads that
-// hold a slab of columns. A row whose tokens lie inside a chunk is finished
-// there; one that crosses chunk borders leaves a partial sum per chunk, and
-// the group of the chunk in which it starts adds them up afterwards.
+// Sorting up to kSortMost tokens in one launch: one cluster of up to 8 blocks
+// holds them all in its shared memory, kThreads * IPT to a block, and sorts them
+// by least-significant-digit radix passes (stable; 9 bits at most a pass, so two
+// for vocabularies below 2^18). Per pass a warp ranks its own items against each
+// other (by the lanes with an equal digit, round after round), the block adds the
+// warps before it, the cluster the blocks before it, and every item is stored at
+// its place, in whichever block that is. The general path's three kernels for
+// every 8 bits took 30 us and more, most of it between the kernels. Bound by the
+// shared-memory round trips and the cluster's barriers.
 // ---------------------------------------------------------------------------
-constexpr int kSumChunk = 32;
-constexpr int kSumThreads = 256;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortMaxBits = 9;
+constexpr int kSortMaxBlocks = 8;
+constexpr int kSortMaxItems = 8;  // a thread's
+constexpr int kSortMost = kSortMaxBlocks * kSortThreads * kSortMaxItems;
 
-// partial sums of chunk c: [2c] of the row that began before it, [2c + 1] of
-// the row that begins in it and goes on after it
-__host__ __device__ inline long long sum_chunks(long long n) {
-  return (n + kSumChunk - 1) / kSumChunk;
+__device__ __forceinline__ int key_of(const void* tokens, int wide, int i, int n, int vocab) {
+  if (i >= n) return vocab;
+  const long long t = token_at(tokens, wide, i);
+  return t >= 0 && t < vocab ? (int)t : vocab;
+}
+
+// Shared memory of a block: items[2][kSortThreads * IPT] (key, place), counts
+// [kSortWarps][1 << bits] (16 bits each), totals, starts.
+struct SortItem {
+  int key, pos;
+};
+inline size_t sort_smem(int ipt, int bits) {
+  return 2 * sizeof(SortItem) * (size_t)kSortThreads * ipt +
+         sizeof(unsigned short) * ((size_t)kSortWarps << bits) + sizeof(int) * (2u << bits) +
+         sizeof(int) * 64;
+}
+
+template <int IPT>
+__global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(
+    int n, int vocab, const void* __restrict__ tokens, int wide, int passes, int bits,
+    int* __restrict__ keyOut, int* __restrict__ posOut) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  grid_dependency_wait();
+  grid_dependency_trigger();
+  namespace cgr = cooperative_groups;
+  cgr::cluster_group cl = cgr::this_cluster();
+  const int blocks = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  constexpr int kTile = kSortThreads * IPT;
+  const int D = 1 << bits, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  SortItem* items = reinterpret_cast<SortItem*>(smem);
+  unsigned short* counts = reinterpret_cast<unsigned short*>(items + 2 * kTile);
+  int* totals = reinterpret_cast<int*>(counts + ((size_t)kSortWarps << bits));
+  int* starts = totals + D;
+  int* sums = starts + D;  // one per warp
+  SortItem it[IPT];
+  const int first = warp * 32 * IPT + lane;  // in the tile: the thread's items are 32 apart
+#pragma unroll
+  for (int r = 0; r < IPT; ++r) {
+    const int i = rank * kTile + first + 32 * r;
+    it[r] = {key_of(tokens, wide, i, n, vocab), i};
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = pass * bits;
+    SortItem* next = items + (pass & 1 ? kTile : 0);
+    if (pass > 0) {
+      const SortItem* prev = items + (pass & 1 ? 0 : kTile);
+#pragma unroll
+      for (int r = 0; r < IPT; ++r) it[r] = prev[first + 32 * r];
+    }
+    for (int i = tid; i < kSortWarps * D / 2; i += kSortThreads)
+      reinterpret_cast<unsigned*>(counts)[i] = 0u;
+    __syncthreads();
+    // rank among the warp's items of the same digit
+    unsigned short* mine = counts + warp * D;
+    int rk[IPT];
+#pragma unroll
+    for (int r = 0; r < IPT; ++r) {
+      const int d = (it[r].key >> shift) & (D - 1);
+      const unsigned peers = __match_any_sync(kFullMask, d);
+      const int before = mine[d];
+      __syncwarp();
+      rk[r] = before + __popc(peers & lanemask_lt());
+      if (lane == __ffs(peers) - 1) mine[d] = (unsigned short)(before + __popc(peers));
+      __syncwarp();
+    }
+    __syncthreads();
+    // counts of the warps before, and the block's totals
+    for (int d = tid; d < D; d += kSortThreads) {
+      int run = 0;
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int c = counts[w * D + d];
+        counts[w * D + d] = (unsigned short)run;
+        run += c;
+      }
+      totals[d] = run;
+    }
+    cl.sync();
+    // where the block's items of each digit start: all smaller digits, and the
+    // same digit in the blocks before
+    int all = 0, before = 0;
+    if (tid < D) {
+#pragma unroll
+      for (int q = 0; q < kSortMaxBlocks; ++q) {
+        const int c = q < blocks ? *cl.map_shared_rank(totals + tid, q) : 0;
+        all += c;
+        before += q < rank ? c : 0;
+      }
+    }
+    int inc = all;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(kFullMask, inc, off);
+      if (lane >= off) inc += o;
+    }
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+      int x = sums[lane];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(kFullMask, x, off);
+        if (lane >= off) x += o;
+      }
+      sums[lane] = x;
+    }
+    __syncthreads();
+    if (tid < D) starts[tid] = inc - all + (warp > 0 ? sums[warp - 1] : 0) + before;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < IPT; ++r) {
+      const int d = (it[r].key >> shift) & (D - 1);
+      const int to = starts[d] + mine[d] + rk[r];
+      if (pass == passes - 1) {
+        if (to < n) {
+          keyOut[to] = it[r].key;
+          posOut[to] = it[r].pos;
+        }
+      } else {
+        *cl.map_shared_rank(next + to % kTile, to / kTile) = it[r];
+      }
+    }
+    cl.sync();  // every item is in place (and no block leaves while it is written to)
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient. The sorted positions are cut into chunks, each summed by one group of
+// G threads that hold a slab of columns, E each. A row whose tokens lie inside a
+// chunk is finished there; one that crosses chunk borders leaves a partial sum
+// per chunk, and the group of the chunk in which it starts adds them up
+// afterwards, in order: nothing depends on the order in which blocks run. When
+// the gradient is overwritten, further blocks of the same launch write zeros into
+// the rows that no token names. Bound by the bytes of g and of the gradient.
+// ---------------------------------------------------------------------------
+constexpr int kSumThreads = 256;
+constexpr int kSumChunk = 32;       // positions of a chunk, at most
+constexpr int kSumChunkLeast = 4;
+constexpr int kSumWanted = 608;     // blocks: four for each SM
+constexpr int kZeroRows = 32;       // rows of a zeroing block
+constexpr int kSumRows = 4;         // rows of g in flight, and of partial sums 8
+constexpr int kJoinRows = 8;
+
+struct SumShape {
+  int E, G, chunk;
+  long long chunks, blocksX, slabs;
+};
+// Chunks of 32 positions, shorter ones where those would not fill the GPU
+// (2048 tokens of 1000 columns: 4 positions, XX us against XX with 32).
+SumShape sum_shape(int n, int dim, int E) {
+  SumShape s;
+  s.E = E;
+  const long long lanes = ((long long)dim + E - 1) / E;
+  s.G = 1;
+  while (s.G < kSumThreads && s.G < lanes) s.G *= 2;
+  s.slabs = (lanes + s.G - 1) / s.G;
+  for (s.chunk = kSumChunk;; s.chunk /= 2) {
+    s.chunks = ((long long)n + s.chunk - 1) / s.chunk;
+    s.blocksX = (s.chunks + kSumThreads / s.G - 1) / (kSumThreads / s.G);
+    if (s.chunk == kSumChunkLeast || s.blocksX * s.slabs >= kSumWanted) return s;
+  }
 }
 
 template <class O, int E>
+__device__ __forceinline__ void zero_row(O* row, int dim, int lane) {
+  Pack<O, E> z;
+#pragma unroll
+  for (int e = 0; e < E; ++e) z.v[e] = from_f32<O>(0.0f);
+  for (long long k = (long long)lane * E; k < dim; k += 32 * E)
+    *reinterpret_cast<Pack<O, E>*>(row + k) = z;
+}
+
+// Zeros in those of kZeroRows rows that no token names: 32 threads look one row
+// up each, then each warp writes every eighth.
+template <class O, int E>
+__device__ void zero_rows(long long v0, int n, int vocab, int dim, const int* __restrict__ key,
+                          O* __restrict__ dtable, long long ldd) {
+  __shared__ unsigned named;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp == 0) {
+    const long long v = v0 + lane;
+    int lo = 0, hi = n;
+    while (lo < hi) {
+      const int mid = lo + (hi - lo) / 2;
+      if (key[mid] < v)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    const unsigned found = __ballot_sync(kFullMask, lo < n && key[lo] == v);
+    if (lane == 0) named = found;
+  }
+  __syncthreads();
+  const unsigned there = named;
+  for (int i = warp; i < kZeroRows && v0 + i < vocab; i += kSumThreads / 32)
+    if (!(there >> i & 1u)) zero_row<O, E>(dtable + (v0 + i) * ldd, dim, lane);
+}
+
+template <bool ADD, class O, int E>
 __device__ __forceinline__ void finish_row(O* p, const float (&acc)[E], float scale,
-                                           int accumulate) {
+                                           const Pack<O, E>& old) {
   Pack<O, E> o;
-  if (accumulate) o = *reinterpret_cast<const Pack<O, E>*>(p);
 #pragma unroll
   for (int e = 0; e < E; ++e)
-    o.v[e] = from_f32<O>(accumulate ? to_f32(o.v[e]) + scale * acc[e] : scale * acc[e]);
+    o.v[e] = from_f32<O>(ADD ? to_f32(old.v[e]) + scale * acc[e] : scale * acc[e]);
   *reinterpret_cast<Pack<O, E>*>(p) = o;
 }
 
-// G lanes (a power of two) hold one slab of a row's columns, E each.
-template <class T, class O, int E>
+// Partial sums of chunk c: part[2c] of the row that began before it, part[2c + 1]
+// of the row that begins in it and goes on after it. Blocks from sumBlocks on
+// (in the first slab) zero rows.
+template <class T, class O, int E, bool ADD>
 __global__ void __launch_bounds__(kSumThreads) k_embed_sum(
-    int n, int vocab, int dim, int G, const int* __restrict__ pos, const int* __restrict__ key,
-    const T* __restrict__ g, long long ldg, float scale, int accumulate, O* __restrict__ dtable,
-    long long ldd, float* __restrict__ part) {
-  constexpr int U = 4;  // rows of g in flight
-  const int perBlock = kSumThreads / G;
-  const long long chunk = (long long)blockIdx.x * perBlock + threadIdx.x / G;
+    int n, int vocab, int dim, int G, int chunkRows, long long chunks, unsigned sumBlocks,
+    const int* __restrict__ pos, const int* __restrict__ key, const T* __restrict__ g,
+    long long ldg, float scale, O* __restrict__ dtable, long long ldd, float* __restrict__ part) {
+  grid_dependency_wait();
+  grid_dependency_trigger();
+  if (blockIdx.x >= sumBlocks) {
+    if (blockIdx.y == 0)
+      zero_rows<O, E>((long long)(blockIdx.x - sumBlocks) * kZeroRows, n, vocab, dim, key,
+                      dtable, ldd);
+    return;
+  }
+  const long long chunk = (long long)blockIdx.x * (kSumThreads / G) + threadIdx.x / G;
   const long long col = ((long long)blockIdx.y * G + threadIdx.x % G) * E;
-  if (chunk >= sum_chunks(n) || col >= dim) return;
-  const long long c0 = chunk * kSumChunk;
-  const long long c1 = min(c0 + kSumChunk, (long long)n);
+  if (chunk >= chunks || col >= dim) return;
+  const int c0 = (int)(chunk * chunkRows);
+  const int c1 = (int)min((long long)c0 + chunkRows, (long long)n);
   int cur = key[c0];
   if (cur >= vocab) return;
   bool openLeft = c0 > 0 && key[c0 - 1] == cur;
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-  auto flush = [&](bool openRight) {
-    if (openLeft || openRight) {
-      float* p = part + (2 * chunk + (openLeft ? 0 : 1)) * dim + col;
+  for (int b = c0; b < c1; b += kSumRows) {
+    Pack<T, E> v[kSumRows];
+    Pack<O, E> old[ADD ? kSumRows : 1];
+    int k[kSumRows + 1];
 #pragma unroll
-      for (int e = 0; e < E; ++e) p[e] = acc[e];
-    } else {
-      finish_row<O, E>(dtable + cur * ldd + col, acc, scale, accumulate);
-    }
-  };
-  bool done = false;
-  for (long long b = c0; b < c1 && !done; b += U) {
-    Pack<T, E> v[U];
-    int k[U];
+    for (int u = 0; u <= kSumRows; ++u) k[u] = b + u < n ? key[b + u] : vocab;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      k[u] = b + u < c1 ? key[b + u] : vocab;
-      if (k[u] < vocab) v[u] = *reinterpret_cast<const Pack<T, E>*>(g + pos[b + u] * ldg + col);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (k[u] >= vocab) {
-        done = true;
-        break;
+    for (int u = 0; u < kSumRows; ++u)
+      if (b + u < c1 && k[u] < vocab) {
+        v[u] = *reinterpret_cast<const Pack<T, E>*>(g + pos[b + u] * ldg + col);
+        // what a row that may end here is added to
+        if (ADD && k[u + 1] != k[u])
+          old[ADD ? u : 0] = *reinterpret_cast<const Pack<O, E>*>(dtable + k[u] * ldd + col);
       }
+#pragma unroll
+    for (int u = 0; u < kSumRows; ++u) {
+      if (b + u >= c1 || k[u] >= vocab) return;
       if (k[u] != cur) {
-        flush(false);
         cur = k[u];
         openLeft = false;
 #pragma unroll
@@ -131,57 +334,62 @@ __global__ void __launch_bounds__(kSumThreads) k_embed_sum(
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] += to_f32(v[u].v[e]);
+      const bool ends = k[u + 1] != cur;
+      if (ends && !openLeft) {
+        finish_row<ADD, O, E>(dtable + cur * ldd + col, acc, scale, old[ADD ? u : 0]);
+      } else if (ends || b + u + 1 == c1) {
+        float* p = part + (2 * chunk + (openLeft ? 0 : 1)) * dim + col;
+#pragma unroll
+        for (int e = 0; e < E; ++e) p[e] = acc[e];
+      }
     }
   }
-  flush(c1 < n && key[c1] == cur);
 }
 
-template <class O, int E>
+template <class O, int E, bool ADD>
 __global__ void __launch_bounds__(kSumThreads) k_embed_join(
-    int n, int vocab, int dim, int G, const int* __restrict__ key,
-    const float* __restrict__ part, float scale, int accumulate, O* __restrict__ dtable,
-    long long ldd) {
-  const int perBlock = kSumThreads / G;
-  const long long chunk = (long long)blockIdx.x * perBlock + threadIdx.x / G;
+    int n, int vocab, int dim, int G, int chunkRows, long long chunks,
+    const int* __restrict__ key, const float* __restrict__ part, float scale,
+    O* __restrict__ dtable, long long ldd) {
+  grid_dependency_wait();
+  grid_dependency_trigger();
+  const long long chunk = (long long)blockIdx.x * (kSumThreads / G) + threadIdx.x / G;
   const long long col = ((long long)blockIdx.y * G + threadIdx.x % G) * E;
-  if (chunk >= sum_chunks(n) || col >= dim) return;
-  const long long c0 = chunk * kSumChunk;
-  long long end = c0 + kSumChunk;
-  if (end >= n) return;
-  const int row = key[end - 1];
-  if (row >= vocab || key[end] != row) return;
+  if (chunk + 1 >= chunks || col >= dim) return;
+  const long long c0 = chunk * chunkRows;
+  const int row = key[c0 + chunkRows - 1];
+  if (row >= vocab || key[c0 + chunkRows] != row) return;
   if (key[c0] == row && c0 > 0 && key[c0 - 1] == row) return;  // starts in an earlier chunk
+  O* const to = dtable + row * ldd + col;
+  Pack<O, E> old;
+  if (ADD) old = *reinterpret_cast<const Pack<O, E>*>(to);
   float acc[E];
   const float* p = part + (2 * chunk + 1) * dim + col;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = p[e];
-  for (long long c = chunk + 1;; ++c) {
-    p = part + 2 * c * dim + col;
+  // the chunks after it that begin with the row, several at a time
+  bool more = true;
+  for (long long c = chunk + 1; more; c += kJoinRows) {
+    Pack<float, E> v[kJoinRows];
+    bool in[kJoinRows];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += p[e];
-    end += kSumChunk;
-    if (end >= n || key[end - 1] != row || key[end] != row) break;
+    for (int u = 0; u < kJoinRows; ++u) in[u] = c + u < chunks && key[(c + u) * chunkRows] == row;
+#pragma unroll
+    for (int u = 0; u < kJoinRows; ++u)
+      if (in[u]) {
+        const float* q = part + 2 * (c + u) * dim + col;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[u].v[e] = q[e];
+      }
+#pragma unroll
+    for (int u = 0; u < kJoinRows; ++u) {
+      more = more && in[u];
+      if (more)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += v[u].v[e];
+    }
   }
-  finish_row<O, E>(dtable + row * ldd + col, acc, scale, accumulate);
-}
-
-// Zeros in the rows that no token names, one warp per row.
-template <class O>
-__global__ void __launch_bounds__(256) k_embed_zero(int n, int vocab, int dim,
-                                                    const int* __restrict__ key,
-                                                    O* __restrict__ dtable, long long ldd) {
-  const long long v = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-  if (v >= vocab) return;
-  long long lo = 0, hi = n;
-  while (lo < hi) {
-    const long long mid = (lo + hi) / 2;
-    if (key[mid] < v)
-      lo = mid + 1;
-    else
-      hi = mid;
-  }
-  if (lo < n && key[lo] == v) return;
-  for (int k = threadIdx.x % 32; k < dim; k += 32) dtable[v * ldd + k] = from_f32<O>(0.0f);
+  finish_row<ADD, O, E>(to, acc, scale, old);
 }
 
 struct GradWork {
@@ -190,9 +398,51 @@ struct GradWork {
 GradWork grad_work(int vocab, int dim, int n) {
   GradWork w{0, 0};
   if (vocab <= 0 || dim <= 0 || n <= 0) return w;
-  w.sortBytes = ((long long)token_sort_scratch_bytes(n, vocab) + 255) & ~255LL;
-  w.partBytes = 2 * sum_chunks(n) * (long long)dim * 4;
+  w.sortBytes = n <= kSortMost ? 2LL * n * (long long)sizeof(int)
+                               : (long long)token_sort_scratch_bytes(n, vocab);
+  w.sortBytes = (w.sortBytes + 255) & ~255LL;
+  for (const int E : {8, 1}) {  // whichever the pointers will allow
+    const long long b = 2 * sum_shape(n, dim, E).chunks * (long long)dim * 4;
+    w.partBytes = b > w.partBytes ? b : w.partBytes;
+  }
   return w;
+}
+
+// Sorts up to kSortMost tokens.
+template <int IPT>
+cudaError_t launch_sort(int n, int vocab, const void* tokens, int wide, int blocks, int* key,
+                        int* pos, cudaStream_t s) {
+  int keyBits = 1;
+  while (keyBits < 31 && (1LL << keyBits) <= vocab) ++keyBits;
+  const int passes = (keyBits + kSortMaxBits - 1) / kSortMaxBits;
+  const int bits = (keyBits + passes - 1) / passes;
+  static std::atomic<unsigned long long> ready{0};  // devices, one word per kernel
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(ready.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(k_embed_sort<IPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sort_smem(IPT, kSortMaxBits));
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = sort_smem(IPT, bits);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)blocks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, k_embed_sort<IPT>, n, vocab, tokens, wide, passes, bits, key, pos);
+  note_launches(1);
+  return e;
 }
 
 }  // namespace
@@ -280,44 +530,53 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
   int st = check_current_device_ptrs(ptrs, nTokens > 0 ? 4 : 3);
   if (st != SPMV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(d_work) + w.sortBytes);
   const int *pos = nullptr, *key = nullptr;
-  if (nTokens > 0) {
+  if (nTokens > kSortMost) {
     st = record_cuda(launch_token_sort(nTokens, vocab, d_tokens, indexBytes, d_work, &pos, &key,
                                        s));
-    if (st != SPMV_OK) return st;
+  } else if (nTokens > 0) {
+    int* k = static_cast<int*>(d_work);
+    // as few items to a thread as the cluster's blocks allow
+    int blocks = 1, ipt = 1;
+    while (blocks < kSortMaxBlocks && blocks * kSortThreads < nTokens) blocks *= 2;
+    while (blocks * kSortThreads * ipt < nTokens) ipt *= 2;
+    const auto sort = ipt == 1   ? launch_sort<1>
+                      : ipt == 2 ? launch_sort<2>
+                      : ipt == 4 ? launch_sort<4>
+                                 : launch_sort<8>;
+    st = record_cuda(sort(nTokens, vocab, d_tokens, indexBytes == 8, blocks, k, k + nTokens, s));
+    key = k;
+    pos = k + nTokens;
   }
-  float* part = reinterpret_cast<float*>(static_cast<char*>(d_work) + w.sortBytes);
+  if (st != SPMV_OK) return st;
+  const int gb = dtype_bytes(gType), tb = dtype_bytes(tableType);
+  const bool wide = dim % 8 == 0 && ld_g * gb % 16 == 0 && ld_dtable * tb % 16 == 0 &&
+                    aligned16(d_g) && aligned16(d_dtable);
+  const SumShape shape = sum_shape(nTokens, dim, wide ? 8 : 1);
+  const long long zeroBlocks = accumulate ? 0 : ((long long)vocab + kZeroRows - 1) / kZeroRows;
+  const dim3 grid((unsigned)(shape.blocksX + zeroBlocks), (unsigned)shape.slabs);
+  if (shape.slabs > 65535 || shape.blocksX + zeroBlocks > 0x7fffffffLL) return SPMV_ERR_TOO_LARGE;
   return record_cuda(with_dtype(gType, [&](auto gv) {
     return with_dtype(tableType, [&](auto ov) {
       using T = decltype(gv);
       using O = decltype(ov);
       O* dt = static_cast<O*>(d_dtable);
-      if (!accumulate) {
-        k_embed_zero<O><<<(unsigned)(((long long)vocab + 7) / 8), 256, 0, s>>>(
-            nTokens, vocab, dim, key, dt, ld_dtable);
-        note_launches(1);
-      }
-      if (nTokens == 0) return cudaGetLastError();
-      auto sum = [&](auto width) {
-        constexpr int E = decltype(width)::value;
-        const long long lanes = (dim + E - 1) / E;
-        int G = 1;
-        while (G < kSumThreads && G < lanes) G *= 2;
-        const dim3 grid((unsigned)((sum_chunks(nTokens) + kSumThreads / G - 1) /
-                                   (kSumThreads / G)),
-                        (unsigned)((lanes + G - 1) / G));
-        k_embed_sum<T, O, E><<<grid, kSumThreads, 0, s>>>(
-            nTokens, vocab, dim, G, pos, key, static_cast<const T*>(d_g), ld_g, scale,
-            accumulate, dt, ld_dtable, part);
-        k_embed_join<O, E><<<grid, kSumThreads, 0, s>>>(nTokens, vocab, dim, G, key, part, scale,
-                                                        accumulate, dt, ld_dtable);
-        note_launches(2);
-        return cudaGetLastError();
-      };
-      const bool wide = dim % 8 == 0 && ld_g % 8 == 0 && ld_dtable % 8 == 0 &&
-                        aligned16(d_g) && aligned16(dt);
-      return wide ? sum(std::integral_constant<int, 8>{})
-                  : sum(std::integral_constant<int, 1>{});
+      const auto sum = accumulate ? (wide ? k_embed_sum<T, O, 8, true> : k_embed_sum<T, O, 1, true>)
+                                  : (wide ? k_embed_sum<T, O, 8, false>
+                                          : k_embed_sum<T, O, 1, false>);
+      cudaError_t e = launch_dependent(
+          sum, grid, kSumThreads, s, (int)nTokens, (int)vocab, (int)dim, shape.G, shape.chunk,
+          shape.chunks, (unsigned)shape.blocksX, pos, key, static_cast<const T*>(d_g),
+          (long long)ld_g, scale, dt, (long long)ld_dtable, part);
+      if (e != cudaSuccess || shape.chunks <= 1) return e;
+      const auto join = accumulate ? (wide ? k_embed_join<O, 8, true> : k_embed_join<O, 1, true>)
+                                   : (wide ? k_embed_join<O, 8, false>
+                                           : k_embed_join<O, 1, false>);
+      return launch_dependent(join, dim3((unsigned)shape.blocksX, (unsigned)shape.slabs),
+                              kSumThreads, s, (int)nTokens, (int)vocab, (int)dim, shape.G,
+                              shape.chunk, shape.chunks, key, (const float*)part, scale, dt,
+                              (long long)ld_dtable);
     });
   }));
 }
