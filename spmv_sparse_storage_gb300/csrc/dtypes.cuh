@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "internal.h"
@@ -58,15 +59,32 @@ inline bool misaligned(const void* p, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) != 0;
 }
 
+// The most dynamic shared memory a kernel may ask for, allowed once per device
+// (not during a stream capture: one call outside it comes first).
+struct KernelOnce {
+  std::atomic<unsigned long long> devices{0};
+  cudaError_t allow(const void* kernel, int smem) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (devices.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
+
 // Launches a kernel that may start before the one ahead of it in the stream has
 // ended (it waits for that by itself, grid_dependency_wait, before it touches
 // memory), which hides most of the gap between two short kernels.
 template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s,
-                             A&&... args) {
+cudaError_t launch_dependent_smem(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                                  cudaStream_t s, A&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -76,6 +94,12 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaS
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
   note_launches(1);
   return e;
+}
+
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s,
+                             A&&... args) {
+  return launch_dependent_smem(kernel, grid, threads, 0, s, static_cast<A&&>(args)...);
 }
 
 // E consecutive elements as one aligned access of E * sizeof(T) bytes (a

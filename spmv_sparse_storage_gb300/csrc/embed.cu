@@ -6,8 +6,6 @@
 // scale times the sum of the rows of g whose token is v.
 #include <cooperative_groups.h>
 
-#include <atomic>
-
 #include "dtypes.cuh"
 #include "device_util.cuh"
 #include "internal.h"
@@ -61,11 +59,12 @@ __global__ void __launch_bounds__(256) k_embed(int n, int vocab, int dim, int lo
 // holds them all in its shared memory, kThreads * IPT to a block, and sorts them
 // by least-significant-digit radix passes (stable; 9 bits at most a pass, so two
 // for vocabularies below 2^18). Per pass a warp ranks its own items against each
-// other (by the lanes with an equal digit, round after round), the block adds the
-// warps before it, the cluster the blocks before it, and every item is stored at
-// its place, in whichever block that is. The general path's three kernels for
-// every 8 bits took 30 us and more, most of it between the kernels. Bound by the
-// shared-memory round trips and the cluster's barriers.
+// other (by the lanes with an equal digit, found by a ballot per bit, round after
+// round), the block adds the warps before it, the cluster the blocks before it,
+// and every item is stored at its place, in whichever block that is. Bound by the
+// shared-memory round trips and the cluster's barriers: 9 us for 2048 tokens, 19
+// for 32768 (matching whole digits took 23). The general path launches three
+// kernels for every 8 bits (65537 tokens: 57 us in all against 50 for 65536).
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -94,7 +93,7 @@ inline size_t sort_smem(int ipt, int bits) {
 template <int IPT>
 __global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(
     int n, int vocab, const void* __restrict__ tokens, int wide, int passes, int bits,
-    int* __restrict__ keyOut, int* __restrict__ posOut) {
+    int2* __restrict__ out) {
   extern __shared__ __align__(16) unsigned char smem[];
   grid_dependency_wait();
   grid_dependency_trigger();
@@ -132,7 +131,11 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(
 #pragma unroll
     for (int r = 0; r < IPT; ++r) {
       const int d = (it[r].key >> shift) & (D - 1);
-      const unsigned peers = __match_any_sync(kFullMask, d);
+      unsigned peers = kFullMask;  // the lanes with the same digit, bit by bit
+      for (int b = 0; b < bits; ++b) {
+        const unsigned set = __ballot_sync(kFullMask, d >> b & 1);
+        peers &= d >> b & 1 ? set : ~set;
+      }
       const int before = mine[d];
       __syncwarp();
       rk[r] = before + __popc(peers & lanemask_lt());
@@ -188,10 +191,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(
       const int d = (it[r].key >> shift) & (D - 1);
       const int to = starts[d] + mine[d] + rk[r];
       if (pass == passes - 1) {
-        if (to < n) {
-          keyOut[to] = it[r].key;
-          posOut[to] = it[r].pos;
-        }
+        if (to < n) out[to] = make_int2(it[r].key, it[r].pos);
       } else {
         *cl.map_shared_rank(next + to % kTile, to / kTile) = it[r];
       }
@@ -202,27 +202,38 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(
 
 // ---------------------------------------------------------------------------
 // Gradient. The sorted positions are cut into chunks, each summed by one group of
-// G threads that hold a slab of columns, E each. A row whose tokens lie inside a
-// chunk is finished there; one that crosses chunk borders leaves a partial sum
-// per chunk, and the group of the chunk in which it starts adds them up
-// afterwards, in order: nothing depends on the order in which blocks run. When
-// the gradient is overwritten, further blocks of the same launch write zeros into
-// the rows that no token names. Bound by the bytes of g and of the gradient.
+// G threads that hold a slab of columns, E each. The group in whose chunk a row's
+// tokens begin finishes the row, as far as the end of the next chunk; a row that
+// goes on beyond that leaves a partial sum in every chunk it touches, and a
+// second kernel adds those up. Either way the terms are added in order, a chunk's
+// at a time: nothing depends on the order in which blocks run. When the gradient
+// is overwritten, further blocks of the same launch write zeros into the rows
+// that no token names. Bound by the bytes of g and of the gradient.
 // ---------------------------------------------------------------------------
 constexpr int kSumThreads = 256;
 constexpr int kSumChunk = 32;       // positions of a chunk, at most
 constexpr int kSumChunkLeast = 4;
 constexpr int kSumWanted = 608;     // blocks: four for each SM
-constexpr int kZeroRows = 32;       // rows of a zeroing block
-constexpr int kSumRows = 4;         // rows of g in flight, and of partial sums 8
-constexpr int kJoinRows = 8;
+constexpr int kSumStaged = 1024;    // positions of a block, at most
+constexpr int kZeroRows = 64;       // rows of a zeroing block
+constexpr int kJoinChunks = 4;      // chunks that a block of the second kernel looks at
+constexpr int kJoinRows = 4;        // partial sums in flight there
+
+// The sorted tokens' numbers and places, `stride` ints apart.
+struct SortedTokens {
+  const int* key;
+  const int* pos;
+  int stride;
+  __device__ __forceinline__ int key_at(long long i) const { return __ldg(key + i * stride); }
+  __device__ __forceinline__ int pos_at(long long i) const { return __ldg(pos + i * stride); }
+};
 
 struct SumShape {
   int E, G, chunk;
   long long chunks, blocksX, slabs;
 };
 // Chunks of 32 positions, shorter ones where those would not fill the GPU
-// (2048 tokens of 1000 columns: 4 positions, XX us against XX with 32).
+// (2048 tokens of 1000 columns: 4 positions, 8.4 us against 24 with 32).
 SumShape sum_shape(int n, int dim, int E) {
   SumShape s;
   s.E = E;
@@ -230,7 +241,9 @@ SumShape sum_shape(int n, int dim, int E) {
   s.G = 1;
   while (s.G < kSumThreads && s.G < lanes) s.G *= 2;
   s.slabs = (lanes + s.G - 1) / s.G;
-  for (s.chunk = kSumChunk;; s.chunk /= 2) {
+  s.chunk = kSumChunk;
+  while (kSumThreads / s.G * s.chunk > kSumStaged) s.chunk /= 2;
+  for (;; s.chunk /= 2) {
     s.chunks = ((long long)n + s.chunk - 1) / s.chunk;
     s.blocksX = (s.chunks + kSumThreads / s.G - 1) / (kSumThreads / s.G);
     if (s.chunk == kSumChunkLeast || s.blocksX * s.slabs >= kSumWanted) return s;
@@ -246,30 +259,44 @@ __device__ __forceinline__ void zero_row(O* row, int dim, int lane) {
     *reinterpret_cast<Pack<O, E>*>(row + k) = z;
 }
 
-// Zeros in those of kZeroRows rows that no token names: 32 threads look one row
-// up each, then each warp writes every eighth.
+// The first position of the sorted keys that is not below v, by a warp: 32 places
+// at a time, so that 32768 keys take three rounds.
+__device__ __forceinline__ int lower_bound_warp(const SortedTokens& in, int n, long long v) {
+  const int lane = threadIdx.x & 31;
+  long long lo = 0, hi = n;  // the answer is in [lo, hi]
+  while (lo < hi) {
+    const long long at = lo + (hi - lo) * lane / 32;
+    const unsigned below = __ballot_sync(kFullMask, in.key_at(at) < v);
+    // places 0 .. popc - 1 are below v
+    const int c = __popc(below);
+    if (c == 0) return (int)lo;
+    const long long next = c < 32 ? lo + (hi - lo) * c / 32 : hi;
+    lo = lo + (hi - lo) * (c - 1) / 32 + 1;
+    hi = next;
+  }
+  return (int)lo;
+}
+
+// Zeros in those of kZeroRows rows that no token names.
 template <class O, int E>
-__device__ void zero_rows(long long v0, int n, int vocab, int dim, const int* __restrict__ key,
+__device__ void zero_rows(long long v0, int n, int vocab, int dim, const SortedTokens& in,
                           O* __restrict__ dtable, long long ldd) {
-  __shared__ unsigned named;
+  __shared__ int bound[2];
+  __shared__ unsigned named[kZeroRows / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (warp == 0) {
-    const long long v = v0 + lane;
-    int lo = 0, hi = n;
-    while (lo < hi) {
-      const int mid = lo + (hi - lo) / 2;
-      if (key[mid] < v)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    const unsigned found = __ballot_sync(kFullMask, lo < n && key[lo] == v);
-    if (lane == 0) named = found;
+  if (threadIdx.x < kZeroRows / 32) named[threadIdx.x] = 0u;
+  if (warp < 2) {
+    const int at = lower_bound_warp(in, n, v0 + warp * kZeroRows);
+    if (lane == 0) bound[warp] = at;
   }
   __syncthreads();
-  const unsigned there = named;
+  for (int i = bound[0] + threadIdx.x; i < bound[1]; i += kSumThreads) {
+    const int r = (int)(in.key_at(i) - v0);
+    atomicOr(&named[r >> 5], 1u << (r & 31));
+  }
+  __syncthreads();
   for (int i = warp; i < kZeroRows && v0 + i < vocab; i += kSumThreads / 32)
-    if (!(there >> i & 1u)) zero_row<O, E>(dtable + (v0 + i) * ldd, dim, lane);
+    if (!(named[i >> 5] >> (i & 31) & 1u)) zero_row<O, E>(dtable + (v0 + i) * ldd, dim, lane);
 }
 
 template <bool ADD, class O, int E>
@@ -283,113 +310,249 @@ __device__ __forceinline__ void finish_row(O* p, const float (&acc)[E], float sc
 }
 
 // Partial sums of chunk c: part[2c] of the row that began before it, part[2c + 1]
-// of the row that begins in it and goes on after it. Blocks from sumBlocks on
-// (in the first slab) zero rows.
+// of the row that begins in it. Blocks from sumBlocks on (in the first slab) zero
+// rows. The keys and places of a block's chunks, and the keys around them, wait in
+// shared memory, so that only the rows of g (and those added to) are waited for.
+// A thread's share of a row (16 or 32 bytes, E = 8) is fetched kAhead rows ahead
+// by asynchronous copies into its own place in shared memory, which takes no
+// registers and no barrier; with E = 1, R rows at a time into registers. (4 rows
+// into registers with E = 8 left the kernel waiting: 283 us for 32768 tokens of
+// 4096 bf16 columns into 131072 rows, 196 with the copies.)
+template <class T, class O, bool ADD>
+constexpr int kSlotBytes = 8 * (int)(sizeof(T) + (ADD ? sizeof(O) : 0));
+template <class T, class O, bool ADD>
+constexpr int kAhead = kSlotBytes<T, O, ADD> > 32 ? 4 : 8;
 template <class T, class O, int E, bool ADD>
-__global__ void __launch_bounds__(kSumThreads) k_embed_sum(
+constexpr int kSumSmem = E == 1 ? 0 : kAhead<T, O, ADD> * kSumThreads * kSlotBytes<T, O, ADD>;
+
+template <class T, class O, int E, bool ADD>
+__global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : 3) k_embed_sum(
     int n, int vocab, int dim, int G, int chunkRows, long long chunks, unsigned sumBlocks,
-    const int* __restrict__ pos, const int* __restrict__ key, const T* __restrict__ g,
+    const SortedTokens in, const T* __restrict__ g,
     long long ldg, float scale, O* __restrict__ dtable, long long ldd, float* __restrict__ part) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  constexpr int kKeys = kSumStaged + 2 * kSumChunk + 2;
+  __shared__ int sKey[kKeys], sPos[kSumStaged + kSumChunk];
   grid_dependency_wait();
   grid_dependency_trigger();
   if (blockIdx.x >= sumBlocks) {
     if (blockIdx.y == 0)
-      zero_rows<O, E>((long long)(blockIdx.x - sumBlocks) * kZeroRows, n, vocab, dim, key,
+      zero_rows<O, E>((long long)(blockIdx.x - sumBlocks) * kZeroRows, n, vocab, dim, in,
                       dtable, ldd);
     return;
   }
-  const long long chunk = (long long)blockIdx.x * (kSumThreads / G) + threadIdx.x / G;
+  // keys from one chunk and one position before the block's first chunk to one
+  // chunk and one position past its last: sKey[i - base]
+  const int perBlock = kSumThreads / G;
+  const long long b0 = (long long)blockIdx.x * perBlock * chunkRows;
+  const long long base = b0 - chunkRows - 1;
+  const int held = perBlock * chunkRows;
+  for (int i = threadIdx.x; i < held + 2 * chunkRows + 2; i += kSumThreads) {
+    const long long at = base + i;
+    sKey[i] = at < 0 ? -1 : at < n ? in.key_at(at) : vocab;
+    if (i < held + chunkRows) sPos[i] = b0 + i < n ? in.pos_at(b0 + i) : 0;
+  }
+  __syncthreads();
+  const long long chunk = (long long)blockIdx.x * perBlock + threadIdx.x / G;
   const long long col = ((long long)blockIdx.y * G + threadIdx.x % G) * E;
   if (chunk >= chunks || col >= dim) return;
-  const int c0 = (int)(chunk * chunkRows);
-  const int c1 = (int)min((long long)c0 + chunkRows, (long long)n);
-  int cur = key[c0];
-  if (cur >= vocab) return;
-  bool openLeft = c0 > 0 && key[c0 - 1] == cur;
-  float acc[E];
+  const int here = (threadIdx.x / G) * chunkRows;  // of the block's positions
+  const int* const k = sKey + here + chunkRows + 1;  // k[i]: key of the chunk's position i
+  const int* const at = sPos + here;
+  const int len = (int)min((long long)chunkRows, n - chunk * chunkRows);
+  const int head = k[0], tail = k[len - 1], after = k[len];
+  if (head >= vocab) return;
+  // the head's row began earlier: the chunk before finishes it if it began there
+  // and ends here
+  const bool openLeft = k[-1] == head;
+  const bool skipHead =
+      openLeft && k[-chunkRows - 1] != head && (tail != head || after != head);
+  // the tail's row goes on: finished here if it began here and ends in the next chunk
+  const bool finish =
+      after == tail && !(openLeft && head == tail) && k[len + chunkRows] != tail;
+  const int most = finish ? len + chunkRows : len;
+  int begin = 0;
+  if (skipHead)
+    while (begin < len && k[begin] == head) ++begin;
+  // whether position i is one of this group's
+  auto mine = [&](int i) { return i < most && k[i] < vocab && (i < len || k[i] == tail); };
+  int cur = head;
+  bool open = openLeft;
+  float acc[E], first[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-  for (int b = c0; b < c1; b += kSumRows) {
-    Pack<T, E> v[kSumRows];
-    Pack<O, E> old[ADD ? kSumRows : 1];
-    int k[kSumRows + 1];
+  for (int e = 0; e < E; ++e) acc[e] = first[e] = 0.0f;
+  auto add = [&](int i, const Pack<T, E>& v, const Pack<O, E>& old) {
+    if (k[i] != cur) {
+      cur = k[i];
+      open = false;
 #pragma unroll
-    for (int u = 0; u <= kSumRows; ++u) k[u] = b + u < n ? key[b + u] : vocab;
+      for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    }
+    if (i == len) {  // the next chunk's terms are a sum of their own
 #pragma unroll
-    for (int u = 0; u < kSumRows; ++u)
-      if (b + u < c1 && k[u] < vocab) {
-        v[u] = *reinterpret_cast<const Pack<T, E>*>(g + pos[b + u] * ldg + col);
-        // what a row that may end here is added to
-        if (ADD && k[u + 1] != k[u])
-          old[ADD ? u : 0] = *reinterpret_cast<const Pack<O, E>*>(dtable + k[u] * ldd + col);
+      for (int e = 0; e < E; ++e) {
+        first[e] = acc[e];
+        acc[e] = 0.0f;
       }
+    }
 #pragma unroll
-    for (int u = 0; u < kSumRows; ++u) {
-      if (b + u >= c1 || k[u] >= vocab) return;
-      if (k[u] != cur) {
-        cur = k[u];
-        openLeft = false;
+    for (int e = 0; e < E; ++e) acc[e] += to_f32(v.v[e]);
+    const bool ends = k[i + 1] != cur;
+    if (ends && !open) {
+      if (i >= len)
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+        for (int e = 0; e < E; ++e) acc[e] += first[e];
+      finish_row<ADD, O, E>(dtable + cur * ldd + col, acc, scale, old);
+    } else if (ends || (i + 1 == len && !finish)) {
+      Pack<float, E> p;
+#pragma unroll
+      for (int e = 0; e < E; ++e) p.v[e] = acc[e];
+      *reinterpret_cast<Pack<float, E>*>(part + (2 * chunk + (open ? 0 : 1)) * dim + col) = p;
+    }
+  };
+  if constexpr (E == 8) {
+    constexpr int kD = kAhead<T, O, ADD>, kT = 8 * (int)sizeof(T), kO = 8 * (int)sizeof(O);
+    // slot j of this thread: its share of a row of g, then of the row added to, in
+    // pieces of 16 bytes that lie 16 * kSumThreads apart (no bank conflicts)
+    constexpr int kPieces = kSlotBytes<T, O, ADD> / 16;
+    unsigned char* const own = ring + threadIdx.x * 16;
+    auto slot = [&](int j, int piece) {
+      return own + (size_t)(j * kPieces + piece) * (16 * kSumThreads);
+    };
+    int next = begin;  // the next position to fetch
+    auto fetch = [&](int j) {
+      if (mine(next)) {
+        const unsigned char* from =
+            reinterpret_cast<const unsigned char*>(g + at[next] * ldg + col);
+#pragma unroll
+        for (int q = 0; q < kT / 16; ++q) cp_async16(slot(j, q), from + 16 * q);
+        if (ADD && k[next + 1] != k[next]) {  // what a row that ends here is added to
+          const unsigned char* to =
+              reinterpret_cast<const unsigned char*>(dtable + k[next] * ldd + col);
+#pragma unroll
+          for (int q = 0; q < kO / 16; ++q) cp_async16(slot(j, kT / 16 + q), to + 16 * q);
+        }
       }
+      ++next;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += to_f32(v[u].v[e]);
-      const bool ends = k[u + 1] != cur;
-      if (ends && !openLeft) {
-        finish_row<ADD, O, E>(dtable + cur * ldd + col, acc, scale, old[ADD ? u : 0]);
-      } else if (ends || b + u + 1 == c1) {
-        float* p = part + (2 * chunk + (openLeft ? 0 : 1)) * dim + col;
+    for (int j = 0; j < kD - 1; ++j) fetch(j);
+    int j = 0;
+    for (int i = begin; mine(i); ++i) {
+      fetch(j == 0 ? kD - 1 : j - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kD - 1) : "memory");
+      Pack<T, E> v;
+      Pack<O, E> old;
 #pragma unroll
-        for (int e = 0; e < E; ++e) p[e] = acc[e];
+      for (int q = 0; q < kT / 16; ++q)
+        reinterpret_cast<uint4*>(&v)[q] = *reinterpret_cast<const uint4*>(slot(j, q));
+      if (ADD)
+#pragma unroll
+        for (int q = 0; q < kO / 16; ++q)
+          reinterpret_cast<uint4*>(&old)[q] =
+              *reinterpret_cast<const uint4*>(slot(j, kT / 16 + q));
+      add(i, v, old);
+      j = j + 1 == kD ? 0 : j + 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    constexpr int R = 8;
+    for (int b = begin; mine(b); b += R) {
+      Pack<T, E> v[R];
+      Pack<O, E> old[R];
+#pragma unroll
+      for (int u = 0; u < R; ++u)
+        if (mine(b + u)) {
+          v[u] = *reinterpret_cast<const Pack<T, E>*>(g + at[b + u] * ldg + col);
+          if (ADD && k[b + u + 1] != k[b + u])
+            old[u] = *reinterpret_cast<const Pack<O, E>*>(dtable + k[b + u] * ldd + col);
+        }
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        if (!mine(b + u)) return;
+        add(b + u, v[u], old[u]);
       }
     }
   }
 }
 
+// The rows that go on beyond the chunk after the one they begin in: a block looks
+// at kJoinChunks chunks for the begin of one, and its kSumThreads / L groups of L
+// lanes add a run of the row's partial sums each.
 template <class O, int E, bool ADD>
-__global__ void __launch_bounds__(kSumThreads) k_embed_join(
-    int n, int vocab, int dim, int G, int chunkRows, long long chunks,
-    const int* __restrict__ key, const float* __restrict__ part, float scale,
+__global__ void __launch_bounds__(kSumThreads, 4) k_embed_join(
+    int n, int vocab, int dim, int logL, int chunkRows, long long chunks,
+    const SortedTokens in, const float* __restrict__ part, float scale,
     O* __restrict__ dtable, long long ldd) {
+  __shared__ __align__(16) float sums[kSumThreads * E];
+  __shared__ unsigned begins;
   grid_dependency_wait();
   grid_dependency_trigger();
-  const long long chunk = (long long)blockIdx.x * (kSumThreads / G) + threadIdx.x / G;
-  const long long col = ((long long)blockIdx.y * G + threadIdx.x % G) * E;
-  if (chunk + 1 >= chunks || col >= dim) return;
-  const long long c0 = chunk * chunkRows;
-  const int row = key[c0 + chunkRows - 1];
-  if (row >= vocab || key[c0 + chunkRows] != row) return;
-  if (key[c0] == row && c0 > 0 && key[c0 - 1] == row) return;  // starts in an earlier chunk
-  O* const to = dtable + row * ldd + col;
-  Pack<O, E> old;
-  if (ADD) old = *reinterpret_cast<const Pack<O, E>*>(to);
-  float acc[E];
-  const float* p = part + (2 * chunk + 1) * dim + col;
+  const int L = 1 << logL, groups = kSumThreads >> logL;
+  const int group = threadIdx.x >> logL;
+  const long long col = ((long long)blockIdx.y * L + (threadIdx.x & (L - 1))) * E;
+  const long long chunk0 = (long long)blockIdx.x * kJoinChunks;
+  if (threadIdx.x < 32) {
+    const long long c0 = (chunk0 + threadIdx.x) * chunkRows, c1 = c0 + chunkRows;
+    bool starts = false;
+    if (threadIdx.x < kJoinChunks && c1 + chunkRows < n) {
+      const int row = in.key_at(c1 - 1), head = in.key_at(c0);
+      const int last = c0 > 0 ? in.key_at(c0 - 1) : -1;
+      starts = row < vocab && in.key_at(c1) == row && in.key_at(c1 + chunkRows) == row &&
+               !(head == row && last == row);
+    }
+    const unsigned found = __ballot_sync(kFullMask, starts);
+    if (threadIdx.x == 0) begins = found;
+  }
+  __syncthreads();
+  for (unsigned left = begins; left != 0; left &= left - 1) {
+    const long long chunk = chunk0 + __ffs(left) - 1;
+    const int row = in.key_at((chunk + 1) * chunkRows - 1);
+    // the chunks after it that begin with the row: m of them
+    long long m = 0;
+    for (int found = kSumThreads; found == kSumThreads; m += found) {
+      const long long c = chunk + 1 + m + threadIdx.x;
+      found = __syncthreads_count(c < chunks && in.key_at(c < chunks ? c * chunkRows : 0) == row);
+    }
+    float acc[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = p[e];
-  // the chunks after it that begin with the row, several at a time
-  bool more = true;
-  for (long long c = chunk + 1; more; c += kJoinRows) {
-    Pack<float, E> v[kJoinRows];
-    bool in[kJoinRows];
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    const long long a = chunk + 1 + m * group / groups, b = chunk + 1 + m * (group + 1) / groups;
+    if (col < dim)
+      for (long long c = a; c < b; c += kJoinRows) {
+        Pack<float, E> v[kJoinRows];
 #pragma unroll
-    for (int u = 0; u < kJoinRows; ++u) in[u] = c + u < chunks && key[(c + u) * chunkRows] == row;
+        for (int u = 0; u < kJoinRows; ++u)
+          if (c + u < b)
+            v[u] = *reinterpret_cast<const Pack<float, E>*>(part + 2 * (c + u) * dim + col);
 #pragma unroll
-    for (int u = 0; u < kJoinRows; ++u)
-      if (in[u]) {
-        const float* q = part + 2 * (c + u) * dim + col;
+        for (int u = 0; u < kJoinRows; ++u)
+          if (c + u < b)
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[u].v[e] = q[e];
+            for (int e = 0; e < E; ++e) acc[e] += v[u].v[e];
       }
 #pragma unroll
-    for (int u = 0; u < kJoinRows; ++u) {
-      more = more && in[u];
-      if (more)
+    for (int e = 0; e < E; ++e) sums[threadIdx.x * E + e] = acc[e];
+    for (int half = groups / 2; half > 0; half /= 2) {  // groups 0 .. half - 1 take the others'
+      __syncthreads();
+      if (group < half)
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += v[u].v[e];
+        for (int e = 0; e < E; ++e)
+          sums[threadIdx.x * E + e] += sums[(threadIdx.x + half * L) * E + e];
     }
+    if (group == 0 && col < dim) {
+      O* const to = dtable + row * ldd + col;
+      Pack<O, E> old;
+      if (ADD) old = *reinterpret_cast<const Pack<O, E>*>(to);
+      const Pack<float, E> q =
+          *reinterpret_cast<const Pack<float, E>*>(part + (2 * chunk + 1) * dim + col);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = q.v[e] + sums[threadIdx.x * E + e];
+      finish_row<ADD, O, E>(to, acc, scale, old);
+    }
+    __syncthreads();  // sums is free again
   }
-  finish_row<ADD, O, E>(to, acc, scale, old);
 }
 
 struct GradWork {
@@ -410,22 +573,16 @@ GradWork grad_work(int vocab, int dim, int n) {
 
 // Sorts up to kSortMost tokens.
 template <int IPT>
-cudaError_t launch_sort(int n, int vocab, const void* tokens, int wide, int blocks, int* key,
-                        int* pos, cudaStream_t s) {
+cudaError_t launch_sort(int n, int vocab, const void* tokens, int wide, int blocks, int2* out,
+                        cudaStream_t s) {
   int keyBits = 1;
   while (keyBits < 31 && (1LL << keyBits) <= vocab) ++keyBits;
   const int passes = (keyBits + kSortMaxBits - 1) / kSortMaxBits;
   const int bits = (keyBits + passes - 1) / passes;
-  static std::atomic<unsigned long long> ready{0};  // devices, one word per kernel
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static KernelOnce once;
+  cudaError_t e = once.allow(reinterpret_cast<const void*>(k_embed_sort<IPT>),
+                            (int)sort_smem(IPT, kSortMaxBits));
   if (e != cudaSuccess) return e;
-  if (!(ready.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
-    e = cudaFuncSetAttribute(k_embed_sort<IPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sort_smem(IPT, kSortMaxBits));
-    if (e != cudaSuccess) return e;
-    ready.fetch_or(1ull << (dev & 63), std::memory_order_release);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kSortThreads);
@@ -440,7 +597,7 @@ cudaError_t launch_sort(int n, int vocab, const void* tokens, int wide, int bloc
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, k_embed_sort<IPT>, n, vocab, tokens, wide, passes, bits, key, pos);
+  e = cudaLaunchKernelEx(&cfg, k_embed_sort<IPT>, n, vocab, tokens, wide, passes, bits, out);
   note_launches(1);
   return e;
 }
@@ -531,12 +688,12 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
   if (st != SPMV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* part = reinterpret_cast<float*>(static_cast<char*>(d_work) + w.sortBytes);
-  const int *pos = nullptr, *key = nullptr;
+  SortedTokens sorted{nullptr, nullptr, 1};
   if (nTokens > kSortMost) {
-    st = record_cuda(launch_token_sort(nTokens, vocab, d_tokens, indexBytes, d_work, &pos, &key,
-                                       s));
+    st = record_cuda(launch_token_sort(nTokens, vocab, d_tokens, indexBytes, d_work, &sorted.pos,
+                                       &sorted.key, s));
   } else if (nTokens > 0) {
-    int* k = static_cast<int*>(d_work);
+    int2* const out = static_cast<int2*>(d_work);
     // as few items to a thread as the cluster's blocks allow
     int blocks = 1, ipt = 1;
     while (blocks < kSortMaxBlocks && blocks * kSortThreads < nTokens) blocks *= 2;
@@ -545,9 +702,8 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
                       : ipt == 2 ? launch_sort<2>
                       : ipt == 4 ? launch_sort<4>
                                  : launch_sort<8>;
-    st = record_cuda(sort(nTokens, vocab, d_tokens, indexBytes == 8, blocks, k, k + nTokens, s));
-    key = k;
-    pos = k + nTokens;
+    st = record_cuda(sort(nTokens, vocab, d_tokens, indexBytes == 8, blocks, out, s));
+    sorted = {&out->x, &out->y, 2};
   }
   if (st != SPMV_OK) return st;
   const int gb = dtype_bytes(gType), tb = dtype_bytes(tableType);
@@ -556,7 +712,8 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
   const SumShape shape = sum_shape(nTokens, dim, wide ? 8 : 1);
   const long long zeroBlocks = accumulate ? 0 : ((long long)vocab + kZeroRows - 1) / kZeroRows;
   const dim3 grid((unsigned)(shape.blocksX + zeroBlocks), (unsigned)shape.slabs);
-  if (shape.slabs > 65535 || shape.blocksX + zeroBlocks > 0x7fffffffLL) return SPMV_ERR_TOO_LARGE;
+  // (the second kernel's slabs are of 32 lanes)
+  if (((long long)dim + 32 * shape.E - 1) / (32 * shape.E) > 65535 || shape.blocksX + zeroBlocks > 0x7fffffffLL) return SPMV_ERR_TOO_LARGE;
   return record_cuda(with_dtype(gType, [&](auto gv) {
     return with_dtype(tableType, [&](auto ov) {
       using T = decltype(gv);
@@ -565,17 +722,26 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
       const auto sum = accumulate ? (wide ? k_embed_sum<T, O, 8, true> : k_embed_sum<T, O, 1, true>)
                                   : (wide ? k_embed_sum<T, O, 8, false>
                                           : k_embed_sum<T, O, 1, false>);
-      cudaError_t e = launch_dependent(
-          sum, grid, kSumThreads, s, (int)nTokens, (int)vocab, (int)dim, shape.G, shape.chunk,
-          shape.chunks, (unsigned)shape.blocksX, pos, key, static_cast<const T*>(d_g),
-          (long long)ld_g, scale, dt, (long long)ld_dtable, part);
-      if (e != cudaSuccess || shape.chunks <= 1) return e;
+      const int smem = wide ? (accumulate ? kSumSmem<T, O, 8, true> : kSumSmem<T, O, 8, false>) : 0;
+      static KernelOnce once[2][2];
+      cudaError_t e = once[accumulate][wide].allow(reinterpret_cast<const void*>(sum), smem);
+      if (e != cudaSuccess) return e;
+      e = launch_dependent_smem(
+          sum, grid, kSumThreads, smem, s, (int)nTokens, (int)vocab, (int)dim, shape.G,
+          shape.chunk, shape.chunks, (unsigned)shape.blocksX, sorted,
+          static_cast<const T*>(d_g), (long long)ld_g, scale, dt, (long long)ld_dtable, part);
+      if (e != cudaSuccess || shape.chunks <= 2) return e;
       const auto join = accumulate ? (wide ? k_embed_join<O, 8, true> : k_embed_join<O, 1, true>)
                                    : (wide ? k_embed_join<O, 8, false>
                                            : k_embed_join<O, 1, false>);
-      return launch_dependent(join, dim3((unsigned)shape.blocksX, (unsigned)shape.slabs),
-                              kSumThreads, s, (int)nTokens, (int)vocab, (int)dim, shape.G,
-                              shape.chunk, shape.chunks, key, (const float*)part, scale, dt,
+      const long long lanes = ((long long)dim + shape.E - 1) / shape.E;
+      int logL = 0;
+      while (logL < 5 && (1 << logL) < lanes) ++logL;
+      return launch_dependent(join,
+                              dim3((unsigned)((shape.chunks + kJoinChunks - 1) / kJoinChunks),
+                                   (unsigned)((lanes + (1 << logL) - 1) >> logL)),
+                              kSumThreads, s, (int)nTokens, (int)vocab, (int)dim, logL,
+                              shape.chunk, shape.chunks, sorted, (const float*)part, scale, dt,
                               (long long)ld_dtable);
     });
   }));

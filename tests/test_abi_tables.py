@@ -1,0 +1,147 @@
+"""The dense-table operators' C entries: exported, bound under their names, and
+answering bad arguments before any CUDA call (no GPU needed)."""
+import ctypes as C
+import re
+import os
+
+import pytest
+import torch
+
+from conftest import ROOT
+
+NAMES = ["spmv_q4_quantize", "spmv_q4_run", "spmv_embed", "spmv_embed_q4", "spmv_embed_grad",
+         "spmv_embed_grad_workspace"]
+
+
+@pytest.fixture(scope="module")
+def sp():
+    from conftest import build_library
+    build_library()
+    import spmv_sparse_storage_gb300 as sp
+    return sp
+
+
+def test_declared_exported_and_bound(sp):
+    header = open(os.path.join(ROOT, "include", "spmv.h")).read()
+    lib = C.CDLL(sp.LIB_PATH)
+    for name in NAMES:
+        assert re.search(rf"\bint {name}\(", header), name
+        assert hasattr(lib, name) and callable(getattr(sp, name)) and name in sp.__all__
+    assert sp.DTYPES == {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def q4(sp, rows=4, cols=64, group=32, scale_type=0, codes=4096, ld_codes=32, scales=4096,
+       ld_scales=2, zeros=None, ld_zeros=0):
+    return sp.spmv_q4(rows, cols, group, scale_type, codes, ld_codes, scales, ld_scales, zeros,
+                      ld_zeros)
+
+
+BAD_Q4 = [dict(rows=-1), dict(cols=-1), dict(group=0), dict(group=16), dict(group=96),
+          dict(group=256), dict(scale_type=3), dict(scale_type=-1), dict(ld_codes=31),
+          dict(ld_scales=1), dict(zeros=4096, ld_zeros=1), dict(codes=None), dict(scales=None),
+          dict(scales=4098)]
+
+
+@pytest.mark.parametrize("bad", BAD_Q4)
+def test_bad_matrices(sp, bad):
+    a = C.byref(q4(sp, **bad))
+    p, lib, inv = 1 << 20, sp._lib, sp.SPMV_ERR_INVALID_ARG
+    assert lib.spmv_q4_run(a, 1, 0, p, 64, None, 0, 0, p + 4096, 4, None) == inv
+    assert lib.spmv_q4_quantize(a, 0, p, 64, None, 0, None) == inv
+    assert lib.spmv_embed_q4(a, 1, 4, p, 1.0, 0, p + 4096, 64, None) == inv
+
+
+def test_null_matrix(sp):
+    lib, inv = sp._lib, sp.SPMV_ERR_INVALID_ARG
+    assert lib.spmv_q4_run(None, 1, 0, 64, 64, None, 0, 0, 64, 4, None) == inv
+    assert lib.spmv_q4_quantize(None, 0, 64, 64, None, 0, None) == inv
+    assert lib.spmv_embed_q4(None, 1, 4, 64, 1.0, 0, 64, 64, None) == inv
+
+
+@pytest.mark.parametrize("bad", [
+    dict(n=-1), dict(xt=3), dict(yt=-1), dict(ldx=63), dict(ldy=3), dict(x=None), dict(y=None),
+    dict(x=(1 << 20) + 2), dict(y=(1 << 21) + 2), dict(c=1 << 22, ldc=3), dict(c=(1 << 22) + 1),
+    dict(x=1 << 21), dict(c=(1 << 21) + 8), dict(c=1 << 21, ldc=5, n=2), dict(y=4096)])
+def test_bad_products(sp, bad):
+    """Among them: y over x, c over y but not y itself, y over the codes."""
+    a = dict(n=1, xt=0, x=1 << 20, ldx=64, c=None, ldc=4, yt=0, y=1 << 21, ldy=4)
+    a.update(bad)
+    m = q4(sp)
+    assert sp._lib.spmv_q4_run(C.byref(m), a["n"], a["xt"], a["x"], a["ldx"], a["c"], a["ldc"],
+                               a["yt"], a["y"], a["ldy"], None) == sp.SPMV_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", [dict(wt=5), dict(ldw=63), dict(w=None), dict(w=(1 << 20) + 1),
+                                 dict(back=1 << 21, ldb=63), dict(back=(1 << 20) + 4),
+                                 dict(back=1 << 20, ldb=65), dict(w=4096)])
+def test_bad_conversions(sp, bad):
+    """Among them: the values over W but not W itself, W over the codes."""
+    a = dict(wt=0, w=1 << 20, ldw=64, back=None, ldb=64)
+    a.update(bad)
+    m = q4(sp, scales=8192)
+    assert sp._lib.spmv_q4_quantize(C.byref(m), a["wt"], a["w"], a["ldw"], a["back"], a["ldb"],
+                                    None) == sp.SPMV_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", [
+    dict(vocab=-1), dict(dim=-1), dict(n=-1), dict(tt=3), dict(ot=3), dict(index=1),
+    dict(table=None), dict(tokens=None), dict(out=None), dict(ldt=15), dict(ldo=15),
+    dict(table=(1 << 20) + 2), dict(tokens=(1 << 21) + 2), dict(out=(1 << 22) + 1),
+    dict(out=1 << 20), dict(out=1 << 21)])
+def test_bad_lookups(sp, bad):
+    a = dict(vocab=10, dim=16, tt=0, table=1 << 20, ldt=16, n=4, index=4, tokens=1 << 21, ot=0,
+             out=1 << 22, ldo=16)
+    a.update(bad)
+    assert sp._lib.spmv_embed(a["vocab"], a["dim"], a["tt"], a["table"], a["ldt"], a["n"],
+                              a["index"], a["tokens"], 1.0, a["ot"], a["out"], a["ldo"],
+                              None) == sp.SPMV_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", [
+    dict(vocab=-1), dict(dim=-1), dict(n=-1), dict(gt=3), dict(tt=3), dict(index=3),
+    dict(add=2), dict(g=None), dict(tokens=None), dict(dt=None), dict(work=None), dict(ldg=15),
+    dict(ldd=15), dict(bytes=-1), dict(bytes=16), dict(work=(1 << 24) + 8), dict(g=1 << 23),
+    dict(work=1 << 23), dict(tokens=1 << 23), dict(g=(1 << 20) + 2)])
+def test_bad_gradients(sp, bad):
+    """Among them: g, the tokens or the workspace over the gradient."""
+    a = dict(vocab=10, dim=16, gt=0, g=1 << 20, ldg=16, n=4, index=4, tokens=1 << 22, add=0,
+             tt=0, dt=1 << 23, ldd=16, work=1 << 24, bytes=1 << 20)
+    a.update(bad)
+    assert sp._lib.spmv_embed_grad(
+        a["vocab"], a["dim"], a["gt"], a["g"], a["ldg"], a["n"], a["index"], a["tokens"], 1.0,
+        a["add"], a["tt"], a["dt"], a["ldd"], a["work"], a["bytes"],
+        None) == sp.SPMV_ERR_INVALID_ARG
+
+
+def test_workspace_sizes(sp):
+    assert sp.spmv_embed_grad_workspace(100, 64, 0) == 0
+    assert sp.spmv_embed_grad_workspace(0, 64, 10) == 0
+    sizes = [sp.spmv_embed_grad_workspace(1000, 256, n) for n in (1, 100, 10_000, 65536, 65537,
+                                                                  1_000_000)]
+    assert all(s > 0 for s in sizes)
+    # the partial sums: two rows of fp32 for each 4 tokens at most, and the sort's 16 + bytes
+    for n, s in zip((1, 100, 10_000, 65536, 65537, 1_000_000), sizes):
+        assert 8 * n <= s <= (2 * (n // 4 + 1)) * 256 * 4 + 24 * n + (1 << 21)
+
+
+def test_nothing_to_do_needs_no_arrays(sp):
+    ok, lib = sp.SPMV_OK, sp._lib
+    assert lib.spmv_q4_run(C.byref(q4(sp)), 0, 0, None, 64, None, 0, 0, None, 4, None) == ok
+    empty = q4(sp, rows=0, codes=None, scales=None)
+    assert lib.spmv_q4_run(C.byref(empty), 3, 0, None, 64, None, 0, 0, None, 0, None) == ok
+    assert lib.spmv_q4_quantize(C.byref(empty), 0, None, 64, None, 0, None) == ok
+    assert lib.spmv_embed(10, 16, 0, None, 16, 0, 4, None, 1.0, 0, None, 16, None) == ok
+    assert lib.spmv_embed_grad(10, 16, 0, None, 16, 0, 4, None, 1.0, 1, 0, None, 16, None, 0,
+                               None) == ok
+
+
+def test_binding_refuses_host_tensors_and_wrong_types(sp):
+    t = torch.zeros(4, 32)
+    with pytest.raises(ValueError):
+        sp.spmv_embed(t, torch.zeros(2, dtype=torch.int64), torch.zeros(2, 32))
+    with pytest.raises(ValueError):
+        sp.spmv_q4_run(t, t, 32, t, t)
+    with pytest.raises(ValueError):
+        sp.spmv_q4_quantize(t, t, t, 32)
+    with pytest.raises(ValueError):
+        sp.spmv_embed_grad(t, torch.zeros(4, dtype=torch.int64), t)
