@@ -360,8 +360,8 @@ int spmv_run_csr_noalloc(int32_t numRows, int32_t numCols, int32_t nnz,
  *
  * These calls take the caller's arrays as they are: no handle, nothing kept
  * from one call for the next, nothing allocated, never a synchronisation, so
- * every one of them can be captured into a CUDA graph (after one call outside
- * capture on the device). They run on the current device; every pointer is a
+ * every one of them can be captured into a CUDA graph (after one such call
+ * outside capture on the device, which sets kernel attributes). They run on the current device; every pointer is a
  * device pointer of that device, aligned to its element's size. Leading
  * dimensions (ld...) count elements (codes: bytes) from one row to the next
  * and are at least the row's width; 64-bit offsets throughout. Sums and
@@ -390,10 +390,11 @@ typedef struct {
 } spmv_q4;
 
 /* Convert a dense matrix W (rows x cols of wType, leading dimension ldw) into
- * a->codes, a->scales and, if not NULL, a->zeros. Per group of a row, with the
- * quotient and the rounding (to nearest, ties to even) in fp32:
- *   without zeros: scale = max|w| / 7, zero = 8;
- *   with zeros:    scale = (max(w, 0) - min(w, 0)) / 15,
+ * a->codes, a->scales and, if not NULL, a->zeros. Per group of a row, with
+ * every step in fp32 (1/7 and 1/15 are the nearest fp32 numbers, round is to the
+ * nearest integer, ties to even):
+ *   without zeros: scale = max|w| * (1/7), zero = 8;
+ *   with zeros:    scale = (max(w, 0) - min(w, 0)) * (1/15),
  *                  zero = clamp(round(-min(w, 0) / scale), 0, 15);
  *   scale rounded to scale_type, then code = clamp(round(w / scale) + zero, 0, 15).
  * A scale that rounds to 0 gives codes equal to zero (values 0; zero = 0 where

@@ -79,7 +79,8 @@ def q4_run(values, x, c=None):
 
 def q4_quantize(w, group, scale_type, with_zeros):
     """(codes, scales as float32 values, zeros or None) of a float32 matrix;
-    the quotients and their rounding are in float32, as the operator says."""
+    the factors 1/15 and 1/7, the quotients and their rounding are in float32, as the
+    operator says."""
     w = np.asarray(w, np.float32)
     rows, cols = w.shape
     groups = -(-cols // group)
@@ -92,8 +93,8 @@ def q4_quantize(w, group, scale_type, with_zeros):
             for g in range(groups):
                 part = w[r, g * group:(g + 1) * group]
                 low, high = min(part.min(), f32(0)), max(part.max(), f32(0))
-                raw = f32(f32(high - low) / f32(15)) if with_zeros else f32(
-                    max(high, -low) / f32(7))
+                raw = (f32(f32(high - low) * f32(1 / 15)) if with_zeros
+                       else f32(max(high, -low) * f32(1 / 7)))
                 if not np.all(np.isfinite(part)):
                     raw = f32(np.nan)
                 s = round_to(np.array([raw]), scale_type)[0]

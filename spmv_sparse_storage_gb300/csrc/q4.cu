@@ -53,7 +53,7 @@ __device__ __forceinline__ float quotient(float w, float step, float inv) {
 // lo <= 0 <= hi: the range of a group's weights (a NaN if one of them is).
 template <class S>
 __device__ __forceinline__ GroupCodes group_codes(float lo, float hi, bool zeros, S* scale) {
-  float raw = zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f;
+  float raw = zeros ? (hi - lo) * (1.0f / 15.0f) : fmaxf(hi, -lo) * (1.0f / 7.0f);
   if (!(hi <= kMaxFinite && lo >= -kMaxFinite)) raw = __int_as_float(0x7fc00000);
   *scale = from_f32<S>(raw);
   GroupCodes c;
