@@ -285,6 +285,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_q4_run(const RunArgs p) {
   float* sums = slots + (size_t)(p.maxTiles + kWarps - 1) * slotFloats;
   const int xWord4 = NB * 4;  // 16-byte pieces of x from one code word to the next
   const bool phases = p.phaseSteps < p.stepShare + (p.stepRest > 0 ? 1 : 0);
+  // vectors joined together (measured: 32 against 36 us for 16 of 16384 x 5120; the
+  // other forms lose by it)
+  constexpr int kSet = NT == 1 || kParts > 1 || !ALIGNED ? 1 : 4;
+  const int sets = kSet == 1 ? p.n : (p.n + kSet - 1) / kSet;
   const int rowBytes = a.cols / 2 + a.cols % 2;
   const int groups = (a.cols + G - 1) / G;
   const X* x = static_cast<const X*>(p.x);
@@ -614,36 +618,44 @@ __global__ void __launch_bounds__(kThreads, 2) k_q4_run(const RunArgs p) {
     // What is not finished yet is kept where the first of them was, or with
     // several phases in `sums`.
     const bool last = f0 + p.phaseSteps >= s1;
-    for (int tv = warp; tv < T * p.n; tv += kWarps) {  // a tile and vector, its rows the lanes
-      const int t = p.n == 1 ? tv : tv / p.n, v = tv - t * p.n;
-      const int o = tv * kTileRows + lane;
-      float sum = phases && f0 > s0 ? sums[o] : 0.0f;
-      float* const in = slots + (size_t)t * slotFloats + v * kParts * kTileRows + lane;
+    for (int item = warp; item < T * sets; item += kWarps) {  // a tile and kSet vectors
+      const int t = sets == 1 ? item : item / sets, v0 = (item - t * sets) * kSet;
       const int w0 = fs > 0 ? owner(t * fs, units) : 0;
       const int w1 = fs > 0 ? owner((t + 1) * fs - 1, units) : -1;
+      float* const in = slots + (size_t)t * slotFloats + v0 * kParts * kTileRows + lane;
+      float* const kept = sums + (t * p.n + v0) * kTileRows + lane;
+      const long long r = (long long)(t0 + t) * kTileRows + lane;
+      const bool write = last && p.P == 1 && r < a.rows;
+      float sum[kSet], c[kSet];
+#pragma unroll
+      for (int b = 0; b < kSet; ++b) {
+        c[b] = write && p.c && v0 + b < p.n ? load_y(p.c, p.yType, (v0 + b) * p.ldc + r) : 0.0f;
+        sum[b] = phases && f0 > s0 && v0 + b < p.n ? kept[b * kTileRows] : 0.0f;
+      }
+      auto add = [&](int w) {
+#pragma unroll
+        for (int b = 0; b < kSet; ++b)
+          if (v0 + b < p.n)
+#pragma unroll
+            for (int q = 0; q < kParts; ++q)
+              sum[b] += in[(size_t)w * slotFloats + (b * kParts + q) * kTileRows];
+      };
       if (units >= kWarps) {
 #pragma unroll 4
-        for (int w = w0; w <= w1; ++w)
-#pragma unroll
-          for (int q = 0; q < kParts; ++q) sum += in[(size_t)w * slotFloats + q * kTileRows];
+        for (int w = w0; w <= w1; ++w) add(w);
       } else {
         for (int w = w0; w <= w1; ++w)
-          if (owner(units * w / kWarps, units) == w)  // not an idle one
-#pragma unroll
-            for (int q = 0; q < kParts; ++q) sum += in[(size_t)w * slotFloats + q * kTileRows];
+          if (owner(units * w / kWarps, units) == w) add(w);  // not an idle one
       }
-      if (!last) {
-        sums[o] = sum;
-      } else if (p.P == 1) {
-        const long long r = (long long)(t0 + t) * kTileRows + lane;
-        if (r < a.rows) {
-          if (p.c) sum += load_y(p.c, p.yType, v * p.ldc + r);
-          store_y(p.y, p.yType, v * p.ldy + r, sum);
-        }
-      } else if (phases) {
-        sums[o] = sum;
-      } else {
-        in[(size_t)w0 * slotFloats] = sum;
+#pragma unroll
+      for (int b = 0; b < kSet; ++b) {
+        if (v0 + b >= p.n) break;
+        if (write)
+          store_y(p.y, p.yType, (v0 + b) * p.ldy + r, sum[b] + c[b]);
+        else if (!last || phases)
+          kept[b * kTileRows] = sum[b];
+        else if (p.P > 1)
+          in[(size_t)w0 * slotFloats + b * kParts * kTileRows] = sum[b];
       }
     }
     if (!last) __syncthreads();
@@ -653,27 +665,35 @@ __global__ void __launch_bounds__(kThreads, 2) k_q4_run(const RunArgs p) {
     cgr::cluster_group cl = cgr::this_cluster();
     cl.sync();
     // blocks with one more step than the others put a tile's first warp elsewhere
-    for (int tv = rank * kWarps + warp; tv < T * p.n; tv += kWarps << p.logP) {
-      const int t = p.n == 1 ? tv : tv / p.n, v = tv - t * p.n;
+    const int more = p.stepShare + 1, less = p.stepShare;
+    for (int item = rank * kWarps + warp; item < T * sets; item += kWarps << p.logP) {
+      const int t = sets == 1 ? item : item / sets, v0 = (item - t * sets) * kSet;
       const long long r = (long long)(t0 + t) * kTileRows + lane;
-      const int rest = (v * kParts) * kTileRows + lane;
-      const int more = p.stepShare + 1, less = p.stepShare;
-      float* const here = sums + tv * kTileRows + lane;
-      float* const atMore = slots + (size_t)(t + owner(t * more, T * more)) * slotFloats + rest;
-      float* const atLess = slots + (size_t)(t + owner(t * less, T * less)) * slotFloats + rest;
-      float parts[8];  // all on their way before the first is added
+      float* const here = sums + (t * p.n + v0) * kTileRows + lane;
+      float* const slot0 = slots + (size_t)t * slotFloats + v0 * kParts * kTileRows + lane;
+      float* const atMore = slot0 + (size_t)owner(t * more, T * more) * slotFloats;
+      float* const atLess = slot0 + (size_t)owner(t * less, T * less) * slotFloats;
+      const int apart = phases ? kTileRows : kParts * kTileRows;
+      float part[kSet][8], c[kSet];  // all on their way before the first is added
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        parts[q] = q < p.P ? *cl.map_shared_rank(phases              ? here
-                                                 : q < p.stepRest ? atMore
-                                                                  : atLess, q)
-                           : 0.0f;
-      float sum = parts[0];
+      for (int b = 0; b < kSet; ++b)
+        c[b] = r < a.rows && p.c && v0 + b < p.n ? load_y(p.c, p.yType, (v0 + b) * p.ldc + r)
+                                                 : 0.0f;
 #pragma unroll
-      for (int q = 1; q < 8; ++q) sum += parts[q];
-      if (r < a.rows) {
-        if (p.c) sum += load_y(p.c, p.yType, v * p.ldc + r);
-        store_y(p.y, p.yType, v * p.ldy + r, sum);
+      for (int q = 0; q < 8; ++q) {
+        float* const from = phases ? here : q < p.stepRest ? atMore : atLess;
+#pragma unroll
+        for (int b = 0; b < kSet; ++b)
+          part[b][q] =
+              q < p.P && v0 + b < p.n ? *cl.map_shared_rank(from + b * apart, q) : 0.0f;
+      }
+#pragma unroll
+      for (int b = 0; b < kSet; ++b) {
+        float sum = part[b][0];
+#pragma unroll
+        for (int q = 1; q < 8; ++q) sum += part[b][q];
+        if (r < a.rows && v0 + b < p.n)
+          store_y(p.y, p.yType, (v0 + b) * p.ldy + r, sum + c[b]);
       }
     }
     cl.sync();  // the others may still be reading this block's sums
@@ -721,9 +741,11 @@ cudaError_t launch_one(const RunArgs& args, cudaStream_t s) {
 template <class X, int G, bool ZEROS>
 cudaError_t launch_group(const RunArgs& p, cudaStream_t s) {
   const bool aligned = aligned16(p.a.codes) && (p.a.ld_codes % 16 == 0 || p.a.rows <= 1);
-  if (!aligned) return launch_one<X, G, 2, false, ZEROS>(p, s);
-  return OpOf<X>::kParts * p.n <= 8 ? launch_one<X, G, 1, true, ZEROS>(p, s)
-                                    : launch_one<X, G, 2, true, ZEROS>(p, s);
+  if (OpOf<X>::kParts * p.n <= 8)
+    return aligned ? launch_one<X, G, 1, true, ZEROS>(p, s)
+                   : launch_one<X, G, 1, false, ZEROS>(p, s);
+  return aligned ? launch_one<X, G, 2, true, ZEROS>(p, s)
+                 : launch_one<X, G, 2, false, ZEROS>(p, s);
 }
 
 // Up to vectors_per_pass<X>() vectors in one launch.
