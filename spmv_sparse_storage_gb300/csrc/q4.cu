@@ -84,18 +84,18 @@ __device__ __forceinline__ void rounded_codes(const float (&w)[N], const GroupCo
   }
 }
 
-// The range of the 16 weights of each of the LANES lanes that share a group, in
+// The range of the 8 H weights of each of the LANES lanes that share a group, in
 // pairs for the 16-bit types; NaN wins. hi = max(0, w), lo = min(0, w).
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
-template <int LANES>
-__device__ __forceinline__ void group_range(const Pack<float, 8> (&v)[2], float& lo, float& hi) {
+template <int LANES, int H>
+__device__ __forceinline__ void group_range(const Pack<float, 8> (&v)[H], float& lo, float& hi) {
   float up = 0.0f, down = 0.0f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < H; ++h)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       up = max_nan(up, v[h].v[e]);
@@ -109,12 +109,12 @@ __device__ __forceinline__ void group_range(const Pack<float, 8> (&v)[2], float&
   hi = up;
   lo = -down;
 }
-template <int LANES, class P, class W>
-__device__ __forceinline__ void pair_range(const Pack<W, 8> (&v)[2], float& lo, float& hi) {
+template <int LANES, class P, class W, int H>
+__device__ __forceinline__ void pair_range(const Pack<W, 8> (&v)[H], float& lo, float& hi) {
   const P* p = reinterpret_cast<const P*>(&v);
   P up = p[0], down = p[0];
 #pragma unroll
-  for (int e = 1; e < 8; ++e) {
+  for (int e = 1; e < 4 * H; ++e) {
     up = __hmax2_nan(up, p[e]);
     down = __hmin2_nan(down, p[e]);
   }
@@ -128,12 +128,12 @@ __device__ __forceinline__ void pair_range(const Pack<W, 8> (&v)[2], float& lo, 
   hi = max_nan(to_f32(both.x), 0.0f);
   lo = -max_nan(to_f32(both.y), 0.0f);
 }
-template <int LANES>
-__device__ __forceinline__ void group_range(const Pack<__half, 8> (&v)[2], float& lo, float& hi) {
+template <int LANES, int H>
+__device__ __forceinline__ void group_range(const Pack<__half, 8> (&v)[H], float& lo, float& hi) {
   pair_range<LANES, __half2>(v, lo, hi);
 }
-template <int LANES>
-__device__ __forceinline__ void group_range(const Pack<__nv_bfloat16, 8> (&v)[2], float& lo,
+template <int LANES, int H>
+__device__ __forceinline__ void group_range(const Pack<__nv_bfloat16, 8> (&v)[H], float& lo,
                                             float& hi) {
   pair_range<LANES, __nv_bfloat162>(v, lo, hi);
 }
@@ -199,63 +199,76 @@ __global__ void __launch_bounds__(256) k_q4_quantize_wide(spmv_q4 a, const W* w,
   }
 }
 
-// Any rows: one warp per row and group, two weights of a byte to a lane.
-template <class W, class S>
-__global__ void __launch_bounds__(256) k_q4_quantize(spmv_q4 a, const W* w, long long ldw,
-                                                     W* back, long long ldb) {
+// Any rows: a warp takes 256 columns of a row, read and written element by
+// element in the order of the columns, and turned in shared memory into 8
+// consecutive ones to a lane. (16384 x 4099 bf16 with zero points and values: XX
+// us; two weights to a lane and one group to a warp took 252.)
+constexpr int kAnyWarps = 8;
+template <class W, class S, int G>
+__global__ void __launch_bounds__(32 * kAnyWarps) k_q4_quantize(spmv_q4 a, const W* w,
+                                                                long long ldw, W* back,
+                                                                long long ldb, unsigned sets) {
+  constexpr int LANES = G / 8;
+  __shared__ Pack<W, 8> turned[kAnyWarps][32];
+  __shared__ unsigned words[kAnyWarps][32];
   grid_dependency_wait();
   grid_dependency_trigger();
-  const int groups = (a.cols + a.group - 1) / a.group;
-  const long long id = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x & 31;
-  if (id >= (long long)a.rows * groups) return;
-  const long long r = id / groups;
-  const int gi = (int)(id % groups);
-  const int k0 = gi * a.group, k1 = min(k0 + a.group, a.cols);
-  float v[4];
-  float up = 0.0f, down = 0.0f;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned rows8 = blockIdx.x / sets, set = blockIdx.x - rows8 * sets;
+  const long long row = (long long)rows8 * kAnyWarps + warp;
+  if (row >= a.rows) return;
+  const int col0 = (int)set * 256;
+  const int n = min(a.cols - col0, 256);  // columns here
+  W* const elements = reinterpret_cast<W*>(turned[warp]);
+  W in[8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int k = k0 + 2 * lane + (j & 1) + 64 * (j >> 1);
-    v[j] = k < k1 ? to_f32(w[r * ldw + k]) : 0.0f;
-    up = max_nan(up, v[j]);
-    down = max_nan(down, -v[j]);
-  }
+  for (int i = 0; i < 8; ++i)
+    in[i] = lane + 32 * i < n ? w[row * ldw + col0 + lane + 32 * i] : from_f32<W>(0.0f);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    up = max_nan(up, __shfl_xor_sync(kFullMask, up, off));
-    down = max_nan(down, __shfl_xor_sync(kFullMask, down, off));
-  }
+  for (int i = 0; i < 8; ++i) elements[lane + 32 * i] = in[i];
+  __syncwarp();
+  const Pack<W, 8> v[1] = {turned[warp][lane]};
+  float lo, hi;
+  group_range<LANES>(v, lo, hi);
   S scale;
-  const GroupCodes c = group_codes<S>(-down, up, a.zeros != nullptr, &scale);
-  if (lane == 0) {
-    static_cast<S*>(a.scales)[r * a.ld_scales + gi] = scale;
-    if (a.zeros) a.zeros[r * a.ld_zeros + gi] = (uint8_t)c.zero;
-  }
+  const GroupCodes c = group_codes<S>(lo, hi, a.zeros != nullptr, &scale);
+  const int mine = min(max(n - 8 * lane, 0), 8);  // of the lane's columns
+  float f[8], u[8];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int k = k0 + 2 * lane + 64 * j;
-    if (k >= k1) continue;
-    const float in[2] = {v[2 * j], v[2 * j + 1]};
-    float u[2];
-    rounded_codes<2>(in, c, u);
-    unsigned q[2];
+  for (int e = 0; e < 8; ++e) f[e] = to_f32(v[0].v[e]);
+  rounded_codes<8>(f, c, u);
+  unsigned word = (c.zero - 0x4b400000u) * 0x11111111u;
+  Pack<W, 8> o;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float d = u[i] - kRound;
-      q[i] = k + i < k1 ? (unsigned)((int)d + (int)c.zero) : 0u;
-      if (back && k + i < k1) back[r * ldb + k + i] = from_f32<W>(d * c.step);
-    }
-    a.codes[r * a.ld_codes + k / 2] = (uint8_t)(q[0] | q[1] << 4);
+  for (int e = 0; e < 8; ++e) {
+    word += __float_as_uint(u[e]) << (4 * e);
+    o.v[e] = from_f32<W>((u[e] - kRound) * c.step);
   }
+  words[warp][lane] = mine == 8 ? word : word & ((1u << (4 * mine)) - 1u);
+  if (back) turned[warp][lane] = o;
+  if (lane % LANES == 0 && mine > 0) {
+    const int gi = (col0 + 8 * lane) / G;
+    static_cast<S*>(a.scales)[row * a.ld_scales + gi] = scale;
+    if (a.zeros) a.zeros[row * a.ld_zeros + gi] = (uint8_t)c.zero;
+  }
+  __syncwarp();
+  const uint8_t* const bytes = reinterpret_cast<const uint8_t*>(words[warp]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (lane + 32 * i < (n + 1) / 2)
+      a.codes[row * a.ld_codes + col0 / 2 + lane + 32 * i] = bytes[lane + 32 * i];
+  if (back)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane + 32 * i < n) back[row * ldb + col0 + lane + 32 * i] = elements[lane + 32 * i];
 }
 
 // ---------------------------------------------------------------------------
-// Rows back in dense form: E columns to a lane and load, kRowLoads of them in
+// Rows back in dense form: 8 columns to a lane and load, kRowLoads of them in
 // flight, G lanes to a token and stretch. Bound by the bytes written.
 // ---------------------------------------------------------------------------
 constexpr int kRowLoads = 4;
-template <class O, int E>
+template <class O>
 __global__ void __launch_bounds__(256) k_embed_q4(spmv_q4 a, int n, int logG, int logGroup,
                                                   const void* __restrict__ tokens, int wide,
                                                   float scale, O* __restrict__ out,
@@ -269,6 +282,7 @@ __global__ void __launch_bounds__(256) k_embed_q4(spmv_q4 a, int n, int logG, in
                       : wide  ? static_cast<const long long*>(tokens)[t]
                               : (long long)static_cast<const int*>(tokens)[t];
   const bool valid = r >= 0 && r < a.rows;
+  constexpr int E = 8;
   const int k0 = ((int)blockIdx.y * kRowLoads * G + (threadIdx.x & (G - 1))) * E;
   unsigned w[kRowLoads];
   float s[kRowLoads], z[kRowLoads];
@@ -280,7 +294,7 @@ __global__ void __launch_bounds__(256) k_embed_q4(spmv_q4 a, int n, int logG, in
     z[i] = 8.0f;
     if (valid && k < a.cols) {
       const uint8_t* q = a.codes + r * a.ld_codes + k / 2;
-      w[i] = E == 8 ? *reinterpret_cast<const unsigned*>(q) : (unsigned)*q >> (4 * (k & 1));
+      w[i] = *reinterpret_cast<const unsigned*>(q);
       s[i] = scale_at(a.scales, a.scale_type, r * a.ld_scales + (k >> logGroup));
       if (a.zeros) z[i] = (float)a.zeros[r * a.ld_zeros + (k >> logGroup)];
     }
@@ -295,6 +309,54 @@ __global__ void __launch_bounds__(256) k_embed_q4(spmv_q4 a, int n, int logG, in
       o.v[e] = from_f32<O>(valid ? ((float)((w[i] >> (4 * e)) & 15u) - z[i]) * s[i] * scale : 0.0f);
     *reinterpret_cast<Pack<O, E>*>(out + t * ldo + k) = o;
   }
+}
+
+// Any rows: a warp takes 256 columns of a token's row, the codes read byte by byte
+// and the results written element by element, turned in shared memory.
+template <class O>
+__global__ void __launch_bounds__(32 * kAnyWarps) k_embed_q4_any(
+    spmv_q4 a, int n, int logGroup, const void* __restrict__ tokens, int wide, float scale,
+    O* __restrict__ out, long long ldo) {
+  __shared__ Pack<O, 8> turned[kAnyWarps][32];
+  __shared__ unsigned words[kAnyWarps][32];
+  grid_dependency_wait();
+  grid_dependency_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long t = (long long)blockIdx.x * kAnyWarps + warp;
+  if (t >= n) return;
+  const long long r = !tokens ? t
+                      : wide  ? static_cast<const long long*>(tokens)[t]
+                              : (long long)static_cast<const int*>(tokens)[t];
+  const bool valid = r >= 0 && r < a.rows;
+  const int col0 = (int)blockIdx.y * 256;
+  const int m = min(a.cols - col0, 256);  // columns here
+  uint8_t* const bytes = reinterpret_cast<uint8_t*>(words[warp]);
+  float s = 0.0f, z = 8.0f;
+  if (valid) {
+    uint8_t in[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      in[i] = lane + 32 * i < (m + 1) / 2
+                  ? a.codes[r * a.ld_codes + col0 / 2 + lane + 32 * i]
+                  : (uint8_t)0;
+    const int k = min(col0 + 8 * lane, a.cols - 1);
+    s = scale_at(a.scales, a.scale_type, r * a.ld_scales + (k >> logGroup));
+    if (a.zeros) z = (float)a.zeros[r * a.ld_zeros + (k >> logGroup)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bytes[lane + 32 * i] = in[i];
+  }
+  __syncwarp();
+  const unsigned w = words[warp][lane];
+  Pack<O, 8> o;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    o.v[e] = from_f32<O>(valid ? ((float)((w >> (4 * e)) & 15u) - z) * s * scale : 0.0f);
+  turned[warp][lane] = o;
+  __syncwarp();
+  const O* const elements = reinterpret_cast<const O*>(turned[warp]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (lane + 32 * i < m) out[t * ldo + col0 + lane + 32 * i] = elements[lane + 32 * i];
 }
 
 // The host-side checks of a 4-bit matrix: sizes, types and leading dimensions
@@ -450,24 +512,24 @@ int spmv_q4_quantize(const spmv_q4* a, spmv_dtype wType, const void* d_w, int64_
   const bool wide = a->cols % 8 == 0 && aligned16(d_w) && ldw * wb % 16 == 0 &&
                     aligned16(d_back) && (!d_back || ld_back * wb % 16 == 0) &&
                     !misaligned(a->codes, 4) && a->ld_codes % 4 == 0;
-  const long long sets = ((long long)a->cols + 512 * kPieces - 1) / (512 * kPieces);
-  const long long blocks =
-      wide ? ((long long)a->rows + 7) / 8 * sets : (a->rows * groups + 7) / 8;
+  const int columns = wide ? 512 * kPieces : 256;  // of a warp
+  const long long sets = ((long long)a->cols + columns - 1) / columns;
+  const long long blocks = ((long long)a->rows + 7) / 8 * sets;
   if (blocks > 0x7fffffffLL) return SPMV_ERR_TOO_LARGE;
   return record_cuda(with_dtype(wType, [&](auto wv) {
     return with_dtype(a->scale_type, [&](auto sv) {
       using W = decltype(wv);
       using S = decltype(sv);
-      const W* src = static_cast<const W*>(d_w);
-      W* back = static_cast<W*>(d_back);
-      if (!wide)
-        return launch_dependent(k_q4_quantize<W, S>, dim3((unsigned)blocks), 256, s, *a, src,
-                                (long long)ldw, back, (long long)ld_back);
-      auto kernel = a->group == 32   ? k_q4_quantize_wide<W, S, 32>
-                    : a->group == 64 ? k_q4_quantize_wide<W, S, 64>
-                                     : k_q4_quantize_wide<W, S, 128>;
-      return launch_dependent(kernel, dim3((unsigned)blocks), 256, s, *a, src, (long long)ldw,
-                              back, (long long)ld_back, (unsigned)sets);
+      const auto kernel =
+          wide ? (a->group == 32   ? k_q4_quantize_wide<W, S, 32>
+                  : a->group == 64 ? k_q4_quantize_wide<W, S, 64>
+                                   : k_q4_quantize_wide<W, S, 128>)
+               : (a->group == 32   ? k_q4_quantize<W, S, 32>
+                  : a->group == 64 ? k_q4_quantize<W, S, 64>
+                                   : k_q4_quantize<W, S, 128>);
+      return launch_dependent(kernel, dim3((unsigned)blocks), 256, s, *a,
+                              static_cast<const W*>(d_w), (long long)ldw,
+                              static_cast<W*>(d_back), (long long)ld_back, (unsigned)sets);
     });
   }));
 }
@@ -552,19 +614,24 @@ int spmv_embed_q4(const spmv_q4* a, int32_t nTokens, int32_t indexBytes, const v
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool wide = a->cols % 8 == 0 && aligned16(d_out) && ld_out * ob % 16 == 0 &&
                     !misaligned(a->codes, 4) && a->ld_codes % 4 == 0;
-  const int E = wide ? 8 : 1;
-  const long long pieces = ((long long)a->cols + E - 1) / E;
+  const int logGroup = a->group == 32 ? 5 : a->group == 64 ? 6 : 7;
+  const long long pieces = ((long long)a->cols + 7) / 8;
   int logG = 0;
   while (logG < 5 && (kRowLoads << logG) < pieces) ++logG;
-  const long long y = (pieces + (kRowLoads << logG) - 1) / (kRowLoads << logG);
+  const int each = wide ? 256 >> logG : kAnyWarps;  // tokens of a block
+  const long long y = wide ? (pieces + (kRowLoads << logG) - 1) / (kRowLoads << logG)
+                           : ((long long)a->cols + 255) / 256;
   if (y > 65535) return SPMV_ERR_TOO_LARGE;
-  const dim3 grid((unsigned)(((long long)nTokens + (256 >> logG) - 1) / (256 >> logG)), (unsigned)y);
-  const int logGroup = a->group == 32 ? 5 : a->group == 64 ? 6 : 7;
+  const dim3 grid((unsigned)(((long long)nTokens + each - 1) / each), (unsigned)y);
   return record_cuda(with_dtype(outType, [&](auto ov) {
     using O = decltype(ov);
-    return launch_dependent(wide ? k_embed_q4<O, 8> : k_embed_q4<O, 1>, grid, 256, s, *a,
-                            (int)nTokens, logG, logGroup, d_tokens, (int)(indexBytes == 8), scale,
-                            static_cast<O*>(d_out), (long long)ld_out);
+    O* out = static_cast<O*>(d_out);
+    return wide ? launch_dependent(k_embed_q4<O>, grid, 256, s, *a, (int)nTokens, logG, logGroup,
+                                   d_tokens, (int)(indexBytes == 8), scale, out,
+                                   (long long)ld_out)
+                : launch_dependent(k_embed_q4_any<O>, grid, 32 * kAnyWarps, s, *a, (int)nTokens,
+                                   logGroup, d_tokens, (int)(indexBytes == 8), scale, out,
+                                   (long long)ld_out);
   }));
 }
 
