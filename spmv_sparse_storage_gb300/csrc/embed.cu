@@ -20,9 +20,11 @@ __device__ __forceinline__ long long token_at(const void* tokens, int wide, long
 
 // ---------------------------------------------------------------------------
 // Lookup: E elements to a lane and load, kRowLoads of them in flight, G lanes to
-// a token and stretch of its row. Bound by the bytes read and written.
+// a token and stretch of its row. Bound by the bytes read and written; with single
+// elements (rows off a 16-byte boundary) by the loads and stores themselves.
 // ---------------------------------------------------------------------------
-constexpr int kRowLoads = 4;
+template <int E>
+constexpr int kRowLoads = E == 1 ? 16 : 4;
 template <class T, class O, int E>
 __global__ void __launch_bounds__(256) k_embed(int n, int vocab, int dim, int logG,
                                                const T* __restrict__ table, long long ldt,
@@ -35,15 +37,15 @@ __global__ void __launch_bounds__(256) k_embed(int n, int vocab, int dim, int lo
   if (t >= n) return;
   const long long token = token_at(tokens, wide, t);
   const bool valid = token >= 0 && token < vocab;
-  const int k0 = ((int)blockIdx.y * kRowLoads * G + (threadIdx.x & (G - 1))) * E;
-  Pack<T, E> v[kRowLoads];
+  const int k0 = ((int)blockIdx.y * kRowLoads<E> * G + (threadIdx.x & (G - 1))) * E;
+  Pack<T, E> v[kRowLoads<E>];
 #pragma unroll
-  for (int i = 0; i < kRowLoads; ++i) {
+  for (int i = 0; i < kRowLoads<E>; ++i) {
     const int k = k0 + i * G * E;
     if (valid && k < dim) v[i] = *reinterpret_cast<const Pack<T, E>*>(table + token * ldt + k);
   }
 #pragma unroll
-  for (int i = 0; i < kRowLoads; ++i) {
+  for (int i = 0; i < kRowLoads<E>; ++i) {
     const int k = k0 + i * G * E;
     if (k >= dim) break;
     Pack<O, E> o;
@@ -633,9 +635,10 @@ int spmv_embed(int32_t vocab, int32_t dim, spmv_dtype tableType, const void* d_t
                     aligned16(d_out) && ld_out * ob % 16 == 0;
   const int E = wide ? 8 : 1;
   const long long pieces = ((long long)dim + E - 1) / E;
+  const int loads = wide ? kRowLoads<8> : kRowLoads<1>;
   int logG = 0;
-  while (logG < 5 && (kRowLoads << logG) < pieces) ++logG;
-  const long long y = (pieces + (kRowLoads << logG) - 1) / (kRowLoads << logG);
+  while (logG < 5 && (loads << logG) < pieces) ++logG;
+  const long long y = (pieces + (loads << logG) - 1) / (loads << logG);
   if (y > 65535) return SPMV_ERR_TOO_LARGE;
   const dim3 grid((unsigned)(((long long)nTokens + (256 >> logG) - 1) / (256 >> logG)), (unsigned)y);
   return record_cuda(with_dtype(tableType, [&](auto tv) {
