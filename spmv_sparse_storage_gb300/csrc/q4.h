@@ -2,6 +2,7 @@
 #pragma once
 
 #include <atomic>
+#include <mutex>
 
 #include "internal.h"
 
@@ -51,6 +52,7 @@ struct Plan {
 constexpr int kMaxSmem = 227 * 1024;
 struct Residency {
   std::atomic<unsigned long long> devices{0};  // where the attribute is set
+  std::mutex mu;
   // clusters of 1, 2, 4, 8 blocks that run at a time, with 1 or 2 blocks on an SM
   int clusters[4][2] = {};
   cudaError_t ask(const void* kernel);
