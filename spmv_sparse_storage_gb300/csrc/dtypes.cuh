@@ -78,6 +78,9 @@ struct KernelOnce {
 // Launches a kernel that may start before the one ahead of it in the stream has
 // ended (it waits for that by itself, grid_dependency_wait, before it touches
 // memory), which hides most of the gap between two short kernels.
+// Such a kernel is under way while its inputs may still be written, so it reads
+// them by ordinary loads: the read-only path (__ldg, const __restrict__) is for
+// data that nothing writes during the kernel's life.
 template <class... P, class... A>
 cudaError_t launch_dependent_smem(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
                                   cudaStream_t s, A&&... args) {

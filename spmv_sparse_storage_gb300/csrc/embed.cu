@@ -28,9 +28,9 @@ template <int E>
 constexpr int kRowLoads = E == 1 ? 16 : 4;
 template <class T, class O, int E>
 __global__ void __launch_bounds__(256) k_embed(int n, int vocab, int dim, int logG,
-                                               const T* __restrict__ table, long long ldt,
-                                               const void* __restrict__ tokens, int wide,
-                                               float scale, O* __restrict__ out, long long ldo) {
+                                               const T* table, long long ldt,
+                                               const void* tokens, int wide,
+                                               float scale, O* out, long long ldo) {
   grid_dependency_wait();
   grid_dependency_trigger();
   const int G = 1 << logG;
@@ -95,8 +95,8 @@ inline size_t sort_smem(int ipt, int bits) {
 
 template <int IPT>
 __global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(
-    int n, int vocab, const void* __restrict__ tokens, int wide, int passes, int bits,
-    int2* __restrict__ out) {
+    int n, int vocab, const void* tokens, int wide, int passes, int bits,
+    int2* out) {
   extern __shared__ __align__(16) unsigned char smem[];
   grid_dependency_wait();
   grid_dependency_trigger();
@@ -230,8 +230,8 @@ struct SortedTokens {
   const int* key;
   const int* pos;
   int stride;
-  __device__ __forceinline__ int key_at(long long i) const { return __ldg(key + i * stride); }
-  __device__ __forceinline__ int pos_at(long long i) const { return __ldg(pos + i * stride); }
+  __device__ __forceinline__ int key_at(long long i) const { return key[i * stride]; }
+  __device__ __forceinline__ int pos_at(long long i) const { return pos[i * stride]; }
 };
 
 struct SumShape {
@@ -286,7 +286,7 @@ __device__ __forceinline__ int lower_bound_warp(const SortedTokens& in, int n, l
 // Zeros in those of kZeroRows rows that no token names.
 template <class O, int E>
 __device__ void zero_rows(long long v0, int n, int vocab, int dim, const SortedTokens& in,
-                          O* __restrict__ dtable, long long ldd) {
+                          O* dtable, long long ldd) {
   __shared__ int bound[2];
   __shared__ unsigned named[kZeroRows / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -334,8 +334,8 @@ constexpr int kSumSmem = E == 1 ? 0 : kAhead<T, O, ADD> * kSumThreads * kSlotByt
 template <class T, class O, int E, bool ADD>
 __global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : 3) k_embed_sum(
     int n, int vocab, int dim, int G, int chunkRows, long long chunks, unsigned sumBlocks,
-    const SortedTokens in, const T* __restrict__ g,
-    long long ldg, float scale, O* __restrict__ dtable, long long ldd, float* __restrict__ part) {
+    const SortedTokens in, const T* g,
+    long long ldg, float scale, O* dtable, long long ldd, float* part) {
   extern __shared__ __align__(16) unsigned char ring[];
   constexpr int kKeys = kSumStaged + 2 * kSumChunk + 2;
   __shared__ int sKey[kKeys], sPos[kSumStaged + kSumChunk];
@@ -489,8 +489,8 @@ __global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : 3) k_embed_sum(
 template <class O, int E, bool ADD>
 __global__ void __launch_bounds__(kSumThreads, 4) k_embed_join(
     int n, int vocab, int dim, int logL, int chunkRows, long long chunks,
-    const SortedTokens in, const float* __restrict__ part, float scale,
-    O* __restrict__ dtable, long long ldd) {
+    const SortedTokens in, const float* part, float scale,
+    O* dtable, long long ldd) {
   __shared__ __align__(16) float sums[kSumThreads * E];
   __shared__ unsigned begins;
   grid_dependency_wait();

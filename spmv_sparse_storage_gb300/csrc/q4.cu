@@ -275,8 +275,8 @@ __global__ void __launch_bounds__(32 * kAnyWarps) k_q4_quantize(spmv_q4 a, const
 constexpr int kRowLoads = 4;
 template <class O>
 __global__ void __launch_bounds__(256) k_embed_q4(spmv_q4 a, int n, int logG, int logGroup,
-                                                  const void* __restrict__ tokens, int wide,
-                                                  float scale, O* __restrict__ out,
+                                                  const void* tokens, int wide,
+                                                  float scale, O* out,
                                                   long long ldo) {
   grid_dependency_wait();
   grid_dependency_trigger();
@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(256) k_embed_q4(spmv_q4 a, int n, int logG, in
 // and the results written element by element, turned in shared memory.
 template <class O>
 __global__ void __launch_bounds__(32 * kAnyWarps) k_embed_q4_any(
-    spmv_q4 a, int n, int logGroup, const void* __restrict__ tokens, int wide, float scale,
-    O* __restrict__ out, long long ldo) {
+    spmv_q4 a, int n, int logGroup, const void* tokens, int wide, float scale,
+    O* out, long long ldo) {
   __shared__ Pack<O, 8> turned[kAnyWarps][32];
   __shared__ unsigned words[kAnyWarps][32];
   grid_dependency_wait();

@@ -405,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_q4_run(const RunArgs p) {
             if (g + 8 * (sRow0 + i) < rowsLeft && l < groupsLeft) {
               const unsigned char* q = scp + i * scales8;
               sc[st][i][l] = scaleBytes == 4
-                                 ? __ldg(reinterpret_cast<const unsigned*>(q) + l)
-                                 : (unsigned)__ldg(reinterpret_cast<const unsigned short*>(q) + l);
-              if (ZEROS) zr[st][i][l] = __ldg(zp + i * zeros8 + l);
+                                 ? reinterpret_cast<const unsigned*>(q)[l]
+                                 : (unsigned)reinterpret_cast<const unsigned short*>(q)[l];
+              if (ZEROS) zr[st][i][l] = zp[i * zeros8 + l];
             }
           }
         --cleft;
