@@ -148,6 +148,26 @@ def test_gradient_of_many_tokens(sp, n, vocab, kind):
     assert torch.equal(dt, again)  # bit for bit
 
 
+@pytest.mark.parametrize("kind", ["uniform", "skewed", "one", "ends"])
+@pytest.mark.parametrize("n", [127, 128, 129, 2047, 2048, 2049, 4096, 8192, 8193, 20000])
+def test_gradient_where_the_way_of_sorting_changes(sp, kind, n):
+    """Lengths around those at which tokens are sorted another way; vocabulary
+    numbers up to the largest and 64-bit tokens that wrap around to small ones."""
+    rng = np.random.default_rng(n)
+    vocab, dim = 2 ** 18 + 3, 8
+    tokens = tokens_of(kind, n, vocab, rng)
+    tokens[::97] = 2 ** 32 + 1
+    tokens[50::97] = -2 ** 63
+    g = ot.round_to(rng.standard_normal((n, dim)), "f16")
+    base = rng.standard_normal((vocab, dim)).astype(np.float32)
+    dt = dev(base, "f32")
+    sp.spmv_embed_grad(dev(g, "f16"), dev(tokens), dt, scale=2.0, accumulate=True)
+    check_grad(host(dt), g, tokens, vocab, 2.0, "f32", base)
+    again = dev(base, "f32")
+    sp.spmv_embed_grad(dev(g, "f16"), dev(tokens), again, scale=2.0, accumulate=True)
+    assert torch.equal(dt, again)  # bit for bit
+
+
 def test_gradient_ignores_what_padding_holds(sp):
     """NaN and infinities in the rows of tokens outside the table, and in the
     gaps between rows, reach nothing."""
