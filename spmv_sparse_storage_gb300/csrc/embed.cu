@@ -5,6 +5,7 @@
 // respect to the table is the transposed product: row v of the gradient is
 // scale times the sum of the rows of g whose token is v.
 #include <cooperative_groups.h>
+#include <algorithm>
 
 #include "dtypes.cuh"
 #include "device_util.cuh"
@@ -18,11 +19,22 @@ __device__ __forceinline__ long long token_at(const void* tokens, int wide, long
               : (long long)static_cast<const int*>(tokens)[i];
 }
 
+// How many elements of every row can be taken at once, `most` (8 or 4), 4 or 1, by
+// accesses of up to 16 bytes.
+inline int elements_at_once(const void* p, long long ld, int dim, int bytes, int most) {
+  for (int E = most; E > 2; E /= 2) {
+    const int access = E * bytes < 16 ? E * bytes : 16;
+    if (dim % E == 0 && !misaligned(p, access) && ld * bytes % access == 0) return E;
+  }
+  return 1;
+}
+
 // ---------------------------------------------------------------------------
 // Lookup: E elements to a lane and load, kRowLoads of them in flight, G lanes to
 // a token and stretch of its row. Bound by the bytes read and written (32768 rows
 // of 4096 fp32 to bf16: 69.8 us, 6.35 TB/s, 0.94 of a copy); with single elements
-// (rows off a 16-byte boundary) by the loads and stores themselves.
+// (rows off a 16-byte boundary) by the loads and stores themselves. 16384 rows of bf16
+// by 8 (4096 columns) 41.5 us, by 4 (4100) 43.6, one by one (4099) 75.
 // ---------------------------------------------------------------------------
 template <int E>
 constexpr int kRowLoads = E == 1 ? 16 : 4;
@@ -140,7 +152,8 @@ __global__ void __launch_bounds__(kRankThreads) k_embed_rank(int n, int vocab, c
 // and every item is stored at its place, in whichever block that is. Bound by the
 // shared-memory round trips and the cluster's barriers: 19 us for 32768 tokens
 // (matching whole digits took 23). The general path launches three
-// kernels for every 8 bits (65537 tokens: 57 us in all against 50 for 65536).
+// kernels for every 8 bits (65537 tokens: 57 us in all against 50 for 65536;
+// a cluster of 16 gained nothing: 67 against 68 us for 131072 tokens).
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -302,14 +315,13 @@ struct SortedTokens {
 };
 
 struct SumShape {
-  int E, G, chunk;
+  int G, chunk;
   long long chunks, blocksX, slabs;
 };
 // Chunks of 32 positions, shorter ones where those would not fill the GPU
 // (2048 tokens of 1000 columns: 4 positions, 8.4 us against 24 with 32).
 SumShape sum_shape(int n, int dim, int E) {
   SumShape s;
-  s.E = E;
   const long long lanes = ((long long)dim + E - 1) / E;
   s.G = 1;
   while (s.G < kSumThreads && s.G < lanes) s.G *= 2;
@@ -386,17 +398,52 @@ __device__ __forceinline__ void finish_row(O* p, const float (&acc)[E], float sc
 // of the row that begins in it. Blocks from sumBlocks on (in the first slab) zero
 // rows. The keys and places of a block's chunks, and the keys around them, wait in
 // shared memory, so that only the rows of g (and those added to) are waited for.
-// A thread's share of a row (16 or 32 bytes, E = 8) is fetched kAhead rows ahead
+// A thread's share of a row (8 to 32 bytes, E = 8 or 4) is fetched kAhead rows ahead
 // by asynchronous copies into its own place in shared memory, which takes no
 // registers and no barrier; with E = 1, R rows at a time into registers. (4 rows
 // into registers with E = 8 left the kernel waiting: 283 us for 32768 tokens of
 // 4096 bf16 columns into 131072 rows, 196 with the copies.)
-template <class T, class O, bool ADD>
-constexpr int kSlotBytes = 8 * (int)(sizeof(T) + (ADD ? sizeof(O) : 0));
-template <class T, class O, bool ADD>
-constexpr int kAhead = kSlotBytes<T, O, ADD> > 32 ? 4 : 8;
+// E is 8 where g and the gradient are both of 16 bits, else 4 at most: 32 bytes to a
+// lane as two pieces would take every sector of a row twice (16384 tokens of fp32 g
+// and gradient, 4096 columns with 8, 4100 with 4: 221 against 169 us; bf16 g 169
+// against 155). Rows that allow 4 alone: 4100 bf16 columns 104 us, element by element
+// 197; 100000 tokens of 300 columns 88 against 144.
+constexpr int sum_most(int gBytes, int tableBytes) {
+  return gBytes == 2 && tableBytes == 2 ? 8 : 4;
+}
 template <class T, class O, int E, bool ADD>
-constexpr int kSumSmem = E == 1 ? 0 : kAhead<T, O, ADD> * kSumThreads * kSlotBytes<T, O, ADD>;
+constexpr int kSlotBytes = E * (int)(sizeof(T) + (ADD ? sizeof(O) : 0));
+template <class T, class O, int E, bool ADD>
+constexpr int kAhead = kSlotBytes<T, O, E, ADD> > 32 ? 4 : 8;
+template <class T, class O, int E, bool ADD>
+constexpr int kSumSmem =
+    E == 1 ? 0 : kAhead<T, O, E, ADD> * kSumThreads * kSlotBytes<T, O, E, ADD>;
+// BYTES of this thread in pieces of 16 (or 8) bytes, each kind of piece of all
+// threads together (no bank conflicts): to shared memory and from there.
+template <int BYTES>
+__device__ __forceinline__ void fetch_share(unsigned char* all, const void* gmem) {
+  constexpr int P = BYTES < 16 ? BYTES : 16;
+#pragma unroll
+  for (int q = 0; q < BYTES / P; ++q) {
+    unsigned char* const to = all + (q * kSumThreads + threadIdx.x) * P;
+    const unsigned char* const from = static_cast<const unsigned char*>(gmem) + P * q;
+    if constexpr (P == 16)
+      cp_async16(to, from);
+    else
+      cp_async_small<P>(to, from);
+  }
+}
+template <class V>
+__device__ __forceinline__ V own_share(const unsigned char* all) {
+  constexpr int BYTES = (int)sizeof(V), P = BYTES < 16 ? BYTES : 16;
+  using Piece = Pack<unsigned, P / 4>;
+  V v;
+#pragma unroll
+  for (int q = 0; q < BYTES / P; ++q)
+    reinterpret_cast<Piece*>(&v)[q] =
+        *reinterpret_cast<const Piece*>(all + (q * kSumThreads + threadIdx.x) * P);
+  return v;
+}
 
 template <class T, class O, int E, bool ADD>
 __global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : 3) k_embed_sum(
@@ -483,28 +530,16 @@ __global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : 3) k_embed_sum(
       *reinterpret_cast<Pack<float, E>*>(part + (2 * chunk + (open ? 0 : 1)) * dim + col) = p;
     }
   };
-  if constexpr (E == 8) {
-    constexpr int kD = kAhead<T, O, ADD>, kT = 8 * (int)sizeof(T), kO = 8 * (int)sizeof(O);
-    // slot j of this thread: its share of a row of g, then of the row added to, in
-    // pieces of 16 bytes that lie 16 * kSumThreads apart (no bank conflicts)
-    constexpr int kPieces = kSlotBytes<T, O, ADD> / 16;
-    unsigned char* const own = ring + threadIdx.x * 16;
-    auto slot = [&](int j, int piece) {
-      return own + (size_t)(j * kPieces + piece) * (16 * kSumThreads);
-    };
+  if constexpr (E > 1) {
+    constexpr int kD = kAhead<T, O, E, ADD>, kT = E * (int)sizeof(T), kO = E * (int)sizeof(O);
+    // slot j: every thread's share of a row of g, then of the row added to
+    auto slot = [&](int j) { return ring + (size_t)j * kSumThreads * kSlotBytes<T, O, E, ADD>; };
     int next = begin;  // the next position to fetch
     auto fetch = [&](int j) {
       if (mine(next)) {
-        const unsigned char* from =
-            reinterpret_cast<const unsigned char*>(g + at[next] * ldg + col);
-#pragma unroll
-        for (int q = 0; q < kT / 16; ++q) cp_async16(slot(j, q), from + 16 * q);
-        if (ADD && k[next + 1] != k[next]) {  // what a row that ends here is added to
-          const unsigned char* to =
-              reinterpret_cast<const unsigned char*>(dtable + k[next] * ldd + col);
-#pragma unroll
-          for (int q = 0; q < kO / 16; ++q) cp_async16(slot(j, kT / 16 + q), to + 16 * q);
-        }
+        fetch_share<kT>(slot(j), g + at[next] * ldg + col);
+        if (ADD && k[next + 1] != k[next])  // what a row that ends here is added to
+          fetch_share<kO>(slot(j) + kSumThreads * kT, dtable + k[next] * ldd + col);
       }
       ++next;
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -515,16 +550,9 @@ __global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : 3) k_embed_sum(
     for (int i = begin; mine(i); ++i) {
       fetch(j == 0 ? kD - 1 : j - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kD - 1) : "memory");
-      Pack<T, E> v;
+      const Pack<T, E> v = own_share<Pack<T, E>>(slot(j));
       Pack<O, E> old;
-#pragma unroll
-      for (int q = 0; q < kT / 16; ++q)
-        reinterpret_cast<uint4*>(&v)[q] = *reinterpret_cast<const uint4*>(slot(j, q));
-      if (ADD)
-#pragma unroll
-        for (int q = 0; q < kO / 16; ++q)
-          reinterpret_cast<uint4*>(&old)[q] =
-              *reinterpret_cast<const uint4*>(slot(j, kT / 16 + q));
+      if (ADD) old = own_share<Pack<O, E>>(slot(j) + kSumThreads * kT);
       add(i, v, old);
       j = j + 1 == kD ? 0 : j + 1;
     }
@@ -637,7 +665,7 @@ GradWork grad_work(int vocab, int dim, int n) {
   w.sortBytes = n <= kSortMost ? 2LL * n * (long long)sizeof(int)
                                : (long long)token_sort_scratch_bytes(n, vocab);
   w.sortBytes = (w.sortBytes + 255) & ~255LL;
-  for (const int E : {8, 1}) {  // whichever the pointers will allow
+  for (const int E : {8, 4, 1}) {  // whichever the pointers will allow
     const long long b = 2 * sum_shape(n, dim, E).chunks * (long long)dim * 4;
     w.partBytes = b > w.partBytes ? b : w.partBytes;
   }
@@ -675,6 +703,30 @@ cudaError_t launch_sort(int n, int vocab, const void* tokens, int wide, int bloc
   return e;
 }
 
+// The sums, zeros and, where a row can go on beyond the next chunk, the join.
+template <class T, class O, int E, bool ADD>
+cudaError_t launch_sums(const SumShape& shape, dim3 grid, int n, int vocab, int dim,
+                        const SortedTokens& sorted, const T* g, long long ldg, float scale,
+                        O* dtable, long long ldd, float* part, cudaStream_t s) {
+  const auto sum = k_embed_sum<T, O, E, ADD>;
+  constexpr int smem = kSumSmem<T, O, E, ADD>;
+  static KernelOnce once;
+  cudaError_t e = once.allow(reinterpret_cast<const void*>(sum), smem);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent_smem(sum, grid, kSumThreads, smem, s, n, vocab, dim, shape.G, shape.chunk,
+                            shape.chunks, (unsigned)shape.blocksX, sorted, g, ldg, scale, dtable,
+                            ldd, part);
+  if (e != cudaSuccess || shape.chunks <= 2) return e;
+  const long long lanes = ((long long)dim + E - 1) / E;
+  int logL = 0;
+  while (logL < 5 && (1 << logL) < lanes) ++logL;
+  return launch_dependent(k_embed_join<O, E, ADD>,
+                          dim3((unsigned)((shape.chunks + kJoinChunks - 1) / kJoinChunks),
+                               (unsigned)((lanes + (1 << logL) - 1) >> logL)),
+                          kSumThreads, s, n, vocab, dim, logL, shape.chunk, shape.chunks, sorted,
+                          (const float*)part, scale, dtable, ldd);
+}
+
 }  // namespace
 }  // namespace spmv
 
@@ -702,11 +754,10 @@ int spmv_embed(int32_t vocab, int32_t dim, spmv_dtype tableType, const void* d_t
   if (st != SPMV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int tb = dtype_bytes(tableType), ob = dtype_bytes(outType);
-  const bool wide = dim % 8 == 0 && aligned16(d_table) && ld_table * tb % 16 == 0 &&
-                    aligned16(d_out) && ld_out * ob % 16 == 0;
-  const int E = wide ? 8 : 1;
+  const int E = std::min(elements_at_once(d_table, ld_table, dim, tb, 8),
+                         elements_at_once(d_out, ld_out, dim, ob, 8));
   const long long pieces = ((long long)dim + E - 1) / E;
-  const int loads = wide ? kRowLoads<8> : kRowLoads<1>;
+  const int loads = E == 1 ? kRowLoads<1> : kRowLoads<8>;
   int logG = 0;
   while (logG < 5 && (loads << logG) < pieces) ++logG;
   const long long y = (pieces + (loads << logG) - 1) / (loads << logG);
@@ -716,8 +767,10 @@ int spmv_embed(int32_t vocab, int32_t dim, spmv_dtype tableType, const void* d_t
     return with_dtype(outType, [&](auto ov) {
       using T = decltype(tv);
       using O = decltype(ov);
-      return launch_dependent(wide ? k_embed<T, O, 8> : k_embed<T, O, 1>, grid, 256, s,
-                              (int)nTokens, (int)vocab, (int)dim, logG,
+      const auto kernel = E == 8   ? k_embed<T, O, 8>
+                          : E == 4 ? k_embed<T, O, 4>
+                                   : k_embed<T, O, 1>;
+      return launch_dependent(kernel, grid, 256, s, (int)nTokens, (int)vocab, (int)dim, logG,
                               static_cast<const T*>(d_table), (long long)ld_table, d_tokens,
                               (int)(indexBytes == 8), scale, static_cast<O*>(d_out),
                               (long long)ld_out);
@@ -787,42 +840,30 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
   }
   if (st != SPMV_OK) return st;
   const int gb = dtype_bytes(gType), tb = dtype_bytes(tableType);
-  const bool wide = dim % 8 == 0 && ld_g * gb % 16 == 0 && ld_dtable * tb % 16 == 0 &&
-                    aligned16(d_g) && aligned16(d_dtable);
-  const SumShape shape = sum_shape(nTokens, dim, wide ? 8 : 1);
+  const int most = sum_most(gb, tb);
+  const int E = std::min(elements_at_once(d_g, ld_g, dim, gb, most),
+                         elements_at_once(d_dtable, ld_dtable, dim, tb, most));
+  const SumShape shape = sum_shape(nTokens, dim, E);
   const long long zeroBlocks = accumulate ? 0 : ((long long)vocab + kZeroRows - 1) / kZeroRows;
   const dim3 grid((unsigned)(shape.blocksX + zeroBlocks), (unsigned)shape.slabs);
   // (the second kernel's slabs are of 32 lanes)
-  if (((long long)dim + 32 * shape.E - 1) / (32 * shape.E) > 65535 || shape.blocksX + zeroBlocks > 0x7fffffffLL) return SPMV_ERR_TOO_LARGE;
+  if (((long long)dim + 32 * E - 1) / (32 * E) > 65535 ||
+      shape.blocksX + zeroBlocks > 0x7fffffffLL)
+    return SPMV_ERR_TOO_LARGE;
   return record_cuda(with_dtype(gType, [&](auto gv) {
     return with_dtype(tableType, [&](auto ov) {
       using T = decltype(gv);
       using O = decltype(ov);
-      O* dt = static_cast<O*>(d_dtable);
-      const auto sum = accumulate ? (wide ? k_embed_sum<T, O, 8, true> : k_embed_sum<T, O, 1, true>)
-                                  : (wide ? k_embed_sum<T, O, 8, false>
-                                          : k_embed_sum<T, O, 1, false>);
-      const int smem = wide ? (accumulate ? kSumSmem<T, O, 8, true> : kSumSmem<T, O, 8, false>) : 0;
-      static KernelOnce once[2][2];
-      cudaError_t e = once[accumulate][wide].allow(reinterpret_cast<const void*>(sum), smem);
-      if (e != cudaSuccess) return e;
-      e = launch_dependent_smem(
-          sum, grid, kSumThreads, smem, s, (int)nTokens, (int)vocab, (int)dim, shape.G,
-          shape.chunk, shape.chunks, (unsigned)shape.blocksX, sorted,
-          static_cast<const T*>(d_g), (long long)ld_g, scale, dt, (long long)ld_dtable, part);
-      if (e != cudaSuccess || shape.chunks <= 2) return e;
-      const auto join = accumulate ? (wide ? k_embed_join<O, 8, true> : k_embed_join<O, 1, true>)
-                                   : (wide ? k_embed_join<O, 8, false>
-                                           : k_embed_join<O, 1, false>);
-      const long long lanes = ((long long)dim + shape.E - 1) / shape.E;
-      int logL = 0;
-      while (logL < 5 && (1 << logL) < lanes) ++logL;
-      return launch_dependent(join,
-                              dim3((unsigned)((shape.chunks + kJoinChunks - 1) / kJoinChunks),
-                                   (unsigned)((lanes + (1 << logL) - 1) >> logL)),
-                              kSumThreads, s, (int)nTokens, (int)vocab, (int)dim, logL,
-                              shape.chunk, shape.chunks, sorted, (const float*)part, scale, dt,
-                              (long long)ld_dtable);
+      constexpr int kMost = sum_most(sizeof(T), sizeof(O));
+      const auto launch = E == kMost ? (accumulate ? launch_sums<T, O, kMost, true>
+                                                   : launch_sums<T, O, kMost, false>)
+                          : E == 4   ? (accumulate ? launch_sums<T, O, 4, true>
+                                                   : launch_sums<T, O, 4, false>)
+                                     : (accumulate ? launch_sums<T, O, 1, true>
+                                                   : launch_sums<T, O, 1, false>);
+      return launch(shape, grid, (int)nTokens, (int)vocab, (int)dim, sorted,
+                    static_cast<const T*>(d_g), (long long)ld_g, scale,
+                    static_cast<O*>(d_dtable), (long long)ld_dtable, part, s);
     });
   }));
 }

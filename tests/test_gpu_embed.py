@@ -168,6 +168,55 @@ def test_gradient_where_the_way_of_sorting_changes(sp, kind, n):
     assert torch.equal(dt, again)  # bit for bit
 
 
+@pytest.mark.parametrize("n,vocab,kind", [(65537, 131072, "skewed"), (131072, 50257, "uniform"),
+                                          (131073, 50257, "uniform"), (100_000, 7, "ends")])
+def test_gradient_of_tokens_beyond_a_cluster(sp, n, vocab, kind):
+    rng = np.random.default_rng(n)
+    tokens = tokens_of(kind, n, vocab, rng)
+    g = ot.round_to(rng.standard_normal((n, 8)), "bf16")
+    dt = torch.full((vocab, 8), float("nan"), device="cuda")
+    sp.spmv_embed_grad(dev(g, "bf16"), dev(tokens), dt)
+    check_grad(host(dt), g, tokens, vocab, 1.0, "f32")
+
+
+@pytest.mark.parametrize("g_type", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("table_type", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim,pad,shift", [(4, 0, 0), (12, 0, 0), (300, 0, 4), (60, 4, 0),
+                                           (1028, 0, 0), (64, 4, 4), (64, 2, 0), (64, 0, 2),
+                                           (2052, 8, 8)])
+def test_rows_on_part_of_a_16_byte_boundary(sp, dim, pad, shift, g_type, table_type):
+    """Rows whose lengths, starts and distances allow 4 elements at a time, or
+    just fail to: lookup, and gradient written and added to."""
+    rng = np.random.default_rng(dim + pad + shift)
+    vocab, n = 40, 150
+
+    def rows(m, kind, a=None):
+        flat = torch.full((shift + m * (dim + pad),), 7.0, dtype=TYPES[kind], device="cuda")
+        t = flat[shift:].view(m, dim + pad)[:, :dim]
+        if a is not None:
+            t.copy_(dev(a))
+        return flat, t
+
+    def untouched(flat, m):
+        gaps = torch.ones(flat.numel(), dtype=torch.bool, device="cuda")
+        gaps[shift:].view(m, dim + pad)[:, :dim] = False
+        return bool(torch.all(flat[gaps] == 7.0))
+
+    tokens = rng.integers(-2, vocab, n)
+    tokens[:70] = 3
+    table = ot.round_to(rng.standard_normal((vocab, dim)), table_type)
+    g = ot.round_to(rng.standard_normal((n, dim)), g_type)
+    flat, out = rows(n, g_type)
+    sp.spmv_embed(rows(vocab, table_type, table)[1], dev(tokens), out, scale=0.7)
+    assert np.array_equal(host(out), ot.embed(table, tokens, 0.7, g_type))
+    assert untouched(flat, n)
+    for add in (False, True):
+        flat, dt = rows(vocab, table_type, table)
+        sp.spmv_embed_grad(rows(n, g_type, g)[1], dev(tokens), dt, scale=1.5, accumulate=add)
+        check_grad(host(dt), g, tokens, vocab, 1.5, table_type, table if add else None)
+        assert untouched(flat, vocab)
+
+
 def test_gradient_ignores_what_padding_holds(sp):
     """NaN and infinities in the rows of tokens outside the table, and in the
     gaps between rows, reach nothing."""
