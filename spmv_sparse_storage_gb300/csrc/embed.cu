@@ -335,13 +335,17 @@ SumShape sum_shape(int n, int dim, int E) {
   }
 }
 
-template <class O, int E>
+// A row of zeros by a warp: 16 bytes at a time between the boundaries it spans.
+template <class O>
 __device__ __forceinline__ void zero_row(O* row, int dim, int lane) {
-  Pack<O, E> z;
-#pragma unroll
-  for (int e = 0; e < E; ++e) z.v[e] = from_f32<O>(0.0f);
-  for (long long k = (long long)lane * E; k < dim; k += 32 * E)
-    *reinterpret_cast<Pack<O, E>*>(row + k) = z;
+  constexpr int E = 16 / (int)sizeof(O);
+  const int head =
+      min(dim, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(O));
+  const int whole = (dim - head) / E;
+  if (lane < head) row[lane] = from_f32<O>(0.0f);
+  uint4* const body = reinterpret_cast<uint4*>(row + head);
+  for (int k = lane; k < whole; k += 32) body[k] = make_uint4(0u, 0u, 0u, 0u);
+  if (lane < dim - head - whole * E) row[head + whole * E + lane] = from_f32<O>(0.0f);
 }
 
 // The first position of the sorted keys that is not below v, by a warp: 32 places
@@ -363,7 +367,7 @@ __device__ __forceinline__ int lower_bound_warp(const SortedTokens& in, int n, l
 }
 
 // Zeros in those of kZeroRows rows that no token names.
-template <class O, int E>
+template <class O>
 __device__ void zero_rows(long long v0, int n, int vocab, int dim, const SortedTokens& in,
                           O* dtable, long long ldd) {
   __shared__ int bound[2];
@@ -381,17 +385,38 @@ __device__ void zero_rows(long long v0, int n, int vocab, int dim, const SortedT
   }
   __syncthreads();
   for (int i = warp; i < kZeroRows && v0 + i < vocab; i += kSumThreads / 32)
-    if (!(named[i >> 5] >> (i & 31) & 1u)) zero_row<O, E>(dtable + (v0 + i) * ldd, dim, lane);
+    if (!(named[i >> 5] >> (i & 31) & 1u)) zero_row(dtable + (v0 + i) * ldd, dim, lane);
 }
 
+// E elements of a row: next to each other, or (APART) `step` apart and of those the
+// ones before `left` (any others are read as the last: loads without a condition are
+// all on their way before the first is waited for).
+template <bool APART, class V, int E>
+__device__ __forceinline__ Pack<V, E> take(const V* p, int step, int left) {
+  Pack<V, E> v;
+  if (!APART) return *reinterpret_cast<const Pack<V, E>*>(p);
+#pragma unroll
+  for (int e = 0; e < E; ++e) v.v[e] = p[min(e * step, left - 1)];
+  return v;
+}
+template <bool APART, class V, int E>
+__device__ __forceinline__ void put(V* p, const Pack<V, E>& v, int step, int left) {
+  if (!APART) {
+    *reinterpret_cast<Pack<V, E>*>(p) = v;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (e * step < left) p[e * step] = v.v[e];
+}
 template <bool ADD, class O, int E>
-__device__ __forceinline__ void finish_row(O* p, const float (&acc)[E], float scale,
-                                           const Pack<O, E>& old) {
+__device__ __forceinline__ Pack<O, E> finished(const float (&acc)[E], float scale,
+                                               const Pack<O, E>& old) {
   Pack<O, E> o;
 #pragma unroll
   for (int e = 0; e < E; ++e)
     o.v[e] = from_f32<O>(ADD ? to_f32(old.v[e]) + scale * acc[e] : scale * acc[e]);
-  *reinterpret_cast<Pack<O, E>*>(p) = o;
+  return o;
 }
 
 // Partial sums of chunk c: part[2c] of the row that began before it, part[2c + 1]
@@ -400,7 +425,10 @@ __device__ __forceinline__ void finish_row(O* p, const float (&acc)[E], float sc
 // shared memory, so that only the rows of g (and those added to) are waited for.
 // A thread's share of a row (8 to 32 bytes, E = 8 or 4) is fetched kAhead rows ahead
 // by asynchronous copies into its own place in shared memory, which takes no
-// registers and no barrier; with E = 1, R rows at a time into registers. (4 rows
+// registers and no barrier. Rows of any alignment (APART) come by single elements, 4
+// to a thread as far apart as the threads of its group, R rows at a time into
+// registers (16384 tokens of 4099 bf16 columns 152 us; one element to a thread, four
+// times the groups, 200; loads under conditions 231). (4 rows
 // into registers with E = 8 left the kernel waiting: 283 us for 32768 tokens of
 // 4096 bf16 columns into 131072 rows, 196 with the copies.)
 // E is 8 where g and the gradient are both of 16 bits, else 4 at most: 32 bytes to a
@@ -417,7 +445,7 @@ template <class T, class O, int E, bool ADD>
 constexpr int kAhead = kSlotBytes<T, O, E, ADD> > 32 ? 4 : 8;
 template <class T, class O, int E, bool ADD>
 constexpr int kSumSmem =
-    E == 1 ? 0 : kAhead<T, O, E, ADD> * kSumThreads * kSlotBytes<T, O, E, ADD>;
+    kAhead<T, O, E, ADD> * kSumThreads * kSlotBytes<T, O, E, ADD>;
 // BYTES of this thread in pieces of 16 (or 8) bytes, each kind of piece of all
 // threads together (no bank conflicts): to shared memory and from there.
 template <int BYTES>
@@ -445,8 +473,8 @@ __device__ __forceinline__ V own_share(const unsigned char* all) {
   return v;
 }
 
-template <class T, class O, int E, bool ADD>
-__global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : 3) k_embed_sum(
+template <class T, class O, int E, bool APART, bool ADD>
+__global__ void __launch_bounds__(kSumThreads, 3) k_embed_sum(
     int n, int vocab, int dim, int G, int chunkRows, long long chunks, unsigned sumBlocks,
     const SortedTokens in, const T* g,
     long long ldg, float scale, O* dtable, long long ldd, float* part) {
@@ -457,8 +485,7 @@ __global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : 3) k_embed_sum(
   grid_dependency_trigger();
   if (blockIdx.x >= sumBlocks) {
     if (blockIdx.y == 0)
-      zero_rows<O, E>((long long)(blockIdx.x - sumBlocks) * kZeroRows, n, vocab, dim, in,
-                      dtable, ldd);
+      zero_rows((long long)(blockIdx.x - sumBlocks) * kZeroRows, n, vocab, dim, in, dtable, ldd);
     return;
   }
   // keys from one chunk and one position before the block's first chunk to one
@@ -474,8 +501,10 @@ __global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : 3) k_embed_sum(
   }
   __syncthreads();
   const long long chunk = (long long)blockIdx.x * perBlock + threadIdx.x / G;
-  const long long col = ((long long)blockIdx.y * G + threadIdx.x % G) * E;
+  const long long col = APART ? (long long)blockIdx.y * G * E + threadIdx.x % G
+                              : ((long long)blockIdx.y * G + threadIdx.x % G) * E;
   if (chunk >= chunks || col >= dim) return;
+  const int columns = dim - (int)col;  // from the thread's first one on
   const int here = (threadIdx.x / G) * chunkRows;  // of the block's positions
   const int* const k = sKey + here + chunkRows + 1;  // k[i]: key of the chunk's position i
   const int* const at = sPos + here;
@@ -522,15 +551,15 @@ __global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : 3) k_embed_sum(
       if (i >= len)
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] += first[e];
-      finish_row<ADD, O, E>(dtable + cur * ldd + col, acc, scale, old);
+      put<APART>(dtable + cur * ldd + col, finished<ADD>(acc, scale, old), G, columns);
     } else if (ends || (i + 1 == len && !finish)) {
       Pack<float, E> p;
 #pragma unroll
       for (int e = 0; e < E; ++e) p.v[e] = acc[e];
-      *reinterpret_cast<Pack<float, E>*>(part + (2 * chunk + (open ? 0 : 1)) * dim + col) = p;
+      put<APART>(part + (2 * chunk + (open ? 0 : 1)) * dim + col, p, G, columns);
     }
   };
-  if constexpr (E > 1) {
+  if constexpr (!APART) {
     constexpr int kD = kAhead<T, O, E, ADD>, kT = E * (int)sizeof(T), kO = E * (int)sizeof(O);
     // slot j: every thread's share of a row of g, then of the row added to
     auto slot = [&](int j) { return ring + (size_t)j * kSumThreads * kSlotBytes<T, O, E, ADD>; };
@@ -558,17 +587,18 @@ __global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : 3) k_embed_sum(
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
-    constexpr int R = 8;
+    constexpr int R = ADD ? 4 : 8;
     for (int b = begin; mine(b); b += R) {
       Pack<T, E> v[R];
       Pack<O, E> old[R];
 #pragma unroll
       for (int u = 0; u < R; ++u)
-        if (mine(b + u)) {
-          v[u] = *reinterpret_cast<const Pack<T, E>*>(g + at[b + u] * ldg + col);
-          if (ADD && k[b + u + 1] != k[b + u])
-            old[u] = *reinterpret_cast<const Pack<O, E>*>(dtable + k[b + u] * ldd + col);
-        }
+        v[u] = take<true, T, E>(g + at[mine(b + u) ? b + u : b] * ldg + col, G, columns);
+      if (ADD)
+#pragma unroll
+        for (int u = 0; u < R; ++u)
+          if (mine(b + u) && k[b + u + 1] != k[b + u])
+            old[u] = take<true, O, E>(dtable + k[b + u] * ldd + col, G, columns);
 #pragma unroll
       for (int u = 0; u < R; ++u) {
         if (!mine(b + u)) return;
@@ -584,8 +614,7 @@ __global__ void __launch_bounds__(kSumThreads, E == 1 ? 4 : 3) k_embed_sum(
 template <class O, int E, bool ADD>
 __global__ void __launch_bounds__(kSumThreads, 4) k_embed_join(
     int n, int vocab, int dim, int logL, int chunkRows, long long chunks,
-    const SortedTokens in, const float* part, float scale,
-    O* dtable, long long ldd) {
+    const SortedTokens in, const float* part, float scale, O* dtable, long long ldd) {
   __shared__ __align__(16) float sums[kSumThreads * E];
   __shared__ unsigned begins;
   grid_dependency_wait();
@@ -650,7 +679,7 @@ __global__ void __launch_bounds__(kSumThreads, 4) k_embed_join(
           *reinterpret_cast<const Pack<float, E>*>(part + (2 * chunk + 1) * dim + col);
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = q.v[e] + sums[threadIdx.x * E + e];
-      finish_row<ADD, O, E>(to, acc, scale, old);
+      *reinterpret_cast<Pack<O, E>*>(to) = finished<ADD>(acc, scale, old);
     }
     __syncthreads();  // sums is free again
   }
@@ -665,7 +694,7 @@ GradWork grad_work(int vocab, int dim, int n) {
   w.sortBytes = n <= kSortMost ? 2LL * n * (long long)sizeof(int)
                                : (long long)token_sort_scratch_bytes(n, vocab);
   w.sortBytes = (w.sortBytes + 255) & ~255LL;
-  for (const int E : {8, 4, 1}) {  // whichever the pointers will allow
+  for (const int E : {8, 4}) {  // whichever the pointers will allow
     const long long b = 2 * sum_shape(n, dim, E).chunks * (long long)dim * 4;
     w.partBytes = b > w.partBytes ? b : w.partBytes;
   }
@@ -703,13 +732,14 @@ cudaError_t launch_sort(int n, int vocab, const void* tokens, int wide, int bloc
   return e;
 }
 
-// The sums, zeros and, where a row can go on beyond the next chunk, the join.
+// The sums, zeros and, where a row can go on beyond the next chunk, the join. With
+// E = 1 (rows of any alignment) a thread of the sums has 4 columns apart.
 template <class T, class O, int E, bool ADD>
 cudaError_t launch_sums(const SumShape& shape, dim3 grid, int n, int vocab, int dim,
                         const SortedTokens& sorted, const T* g, long long ldg, float scale,
                         O* dtable, long long ldd, float* part, cudaStream_t s) {
-  const auto sum = k_embed_sum<T, O, E, ADD>;
-  constexpr int smem = kSumSmem<T, O, E, ADD>;
+  const auto sum = k_embed_sum<T, O, E == 1 ? 4 : E, E == 1, ADD>;
+  constexpr int smem = E == 1 ? 0 : kSumSmem<T, O, E, ADD>;
   static KernelOnce once;
   cudaError_t e = once.allow(reinterpret_cast<const void*>(sum), smem);
   if (e != cudaSuccess) return e;
@@ -843,7 +873,7 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
   const int most = sum_most(gb, tb);
   const int E = std::min(elements_at_once(d_g, ld_g, dim, gb, most),
                          elements_at_once(d_dtable, ld_dtable, dim, tb, most));
-  const SumShape shape = sum_shape(nTokens, dim, E);
+  const SumShape shape = sum_shape(nTokens, dim, std::max(E, 4));
   const long long zeroBlocks = accumulate ? 0 : ((long long)vocab + kZeroRows - 1) / kZeroRows;
   const dim3 grid((unsigned)(shape.blocksX + zeroBlocks), (unsigned)shape.slabs);
   // (the second kernel's slabs are of 32 lanes)
