@@ -293,8 +293,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(
 // is overwritten, further blocks of the same launch write zeros into the rows
 // that no token names. Bound by the bytes of g and of the gradient: 32768 tokens of
 // 4096 bf16 columns into 131072 rows take 199 us here, 6.6 TB/s or 0.97 of a copy,
-// between the sort (19 us) and the second kernel (17 us, which waits on its own
-// barriers).
+// between the sort (19 us) and the second kernel (9 us).
 // ---------------------------------------------------------------------------
 constexpr int kSumThreads = 256;
 constexpr int kSumChunk = 32;       // positions of a chunk, at most
@@ -302,7 +301,8 @@ constexpr int kSumChunkLeast = 4;
 constexpr int kSumWanted = 608;     // blocks: four for each SM
 constexpr int kSumStaged = 1024;    // positions of a block, at most
 constexpr int kZeroRows = 64;       // rows of a zeroing block
-constexpr int kJoinChunks = 4;      // chunks that a block of the second kernel looks at
+constexpr int kJoinChunks = 1024;   // chunks that a block of the second kernel looks at
+constexpr int kJoinBlocks = 32;     // blocks that share the rows found there
 constexpr int kJoinRows = 4;        // partial sums in flight there
 
 // The sorted tokens' numbers and places, `stride` ints apart.
@@ -477,7 +477,8 @@ template <class T, class O, int E, bool APART, bool ADD>
 __global__ void __launch_bounds__(kSumThreads, 3) k_embed_sum(
     int n, int vocab, int dim, int G, int chunkRows, long long chunks, unsigned sumBlocks,
     const SortedTokens in, const T* g,
-    long long ldg, float scale, O* dtable, long long ldd, float* part) {
+    long long ldg, float scale, O* dtable, long long ldd, float* part,
+    unsigned char* goesOn) {
   extern __shared__ __align__(16) unsigned char ring[];
   constexpr int kKeys = kSumStaged + 2 * kSumChunk + 2;
   __shared__ int sKey[kKeys], sPos[kSumStaged + kSumChunk];
@@ -510,6 +511,11 @@ __global__ void __launch_bounds__(kSumThreads, 3) k_embed_sum(
   const int* const at = sPos + here;
   const int len = (int)min((long long)chunkRows, n - chunk * chunkRows);
   const int head = k[0], tail = k[len - 1], after = k[len];
+  // whether the tail's row begins here and goes on beyond the next chunk, for the
+  // second kernel
+  if (col == 0)
+    goesOn[chunk] = tail < vocab && after == tail && k[len + chunkRows] == tail &&
+                    !(k[-1] == head && head == tail);
   if (head >= vocab) return;
   // the head's row began earlier: the chunk before finishes it if it began there
   // and ends here
@@ -608,36 +614,48 @@ __global__ void __launch_bounds__(kSumThreads, 3) k_embed_sum(
   }
 }
 
-// The rows that go on beyond the chunk after the one they begin in: a block looks
-// at kJoinChunks chunks for the begin of one, and its kSumThreads / L groups of L
-// lanes add a run of the row's partial sums each.
+// The rows that go on beyond the chunk after the one they begin in, as the sums have
+// marked them: kJoinBlocks blocks look at the marks of the same kJoinChunks chunks
+// and take the marked ones in turn; a block's kSumThreads / L groups of L lanes add a
+// run of the row's partial sums each. (A block for every 4 chunks, most of which
+// found nothing, 17 us instead of 9 for 32768 tokens of 4096 bf16 columns; 2048 tokens
+// 23.4 -> 17.4 in all. 16 blocks to the same marks 231 us in all, 32 227, 64 226; with
+// 128 lanes to a group the long rows of a vocabulary of 3 take 48 us, with 64 38.)
 template <class O, int E, bool ADD>
 __global__ void __launch_bounds__(kSumThreads, 4) k_embed_join(
-    int n, int vocab, int dim, int logL, int chunkRows, long long chunks,
-    const SortedTokens in, const float* part, float scale, O* dtable, long long ldd) {
+    int dim, int logL, int chunkRows, long long chunks, const SortedTokens in,
+    const unsigned char* goesOn, const float* part, float scale, O* dtable, long long ldd) {
   __shared__ __align__(16) float sums[kSumThreads * E];
-  __shared__ unsigned begins;
+  __shared__ unsigned begins[kJoinChunks / 32];
+  static_assert(kJoinChunks == 32 * 32, "a word of begins to a lane");
   grid_dependency_wait();
   grid_dependency_trigger();
   const int L = 1 << logL, groups = kSumThreads >> logL;
-  const int group = threadIdx.x >> logL;
+  const int group = threadIdx.x >> logL, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long col = ((long long)blockIdx.y * L + (threadIdx.x & (L - 1))) * E;
-  const long long chunk0 = (long long)blockIdx.x * kJoinChunks;
-  if (threadIdx.x < 32) {
-    const long long c0 = (chunk0 + threadIdx.x) * chunkRows, c1 = c0 + chunkRows;
-    bool starts = false;
-    if (threadIdx.x < kJoinChunks && c1 + chunkRows < n) {
-      const int row = in.key_at(c1 - 1), head = in.key_at(c0);
-      const int last = c0 > 0 ? in.key_at(c0 - 1) : -1;
-      starts = row < vocab && in.key_at(c1) == row && in.key_at(c1 + chunkRows) == row &&
-               !(head == row && last == row);
-    }
-    const unsigned found = __ballot_sync(kFullMask, starts);
-    if (threadIdx.x == 0) begins = found;
+  const long long chunk0 = (long long)(blockIdx.x / kJoinBlocks) * kJoinChunks;
+#pragma unroll
+  for (int w = warp; w < kJoinChunks / 32; w += kSumThreads / 32) {
+    const long long c = chunk0 + w * 32 + lane;
+    const unsigned found = __ballot_sync(kFullMask, c < chunks && goesOn[c] != 0);
+    if (lane == 0) begins[w] = found;
   }
   __syncthreads();
-  for (unsigned left = begins; left != 0; left &= left - 1) {
-    const long long chunk = chunk0 + __ffs(left) - 1;
+  // every warp: how many begins there are, and before each word of them
+  const unsigned word = begins[lane];
+  int upTo = __popc(word);
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(kFullMask, upTo, off);
+    if (lane >= off) upTo += o;
+  }
+  const int total = __shfl_sync(kFullMask, upTo, 31);
+  for (int item = blockIdx.x % kJoinBlocks; item < total; item += kJoinBlocks) {
+    const int w = __ffs(__ballot_sync(kFullMask, upTo > item)) - 1;  // it is in this word
+    unsigned bits = __shfl_sync(kFullMask, word, w);
+    for (int skip = item - (__shfl_sync(kFullMask, upTo, w) - __popc(bits)); skip > 0; --skip)
+      bits &= bits - 1;
+    const long long chunk = chunk0 + w * 32 + __ffs(bits) - 1;
     const int row = in.key_at((chunk + 1) * chunkRows - 1);
     // the chunks after it that begin with the row: m of them
     long long m = 0;
@@ -686,17 +704,19 @@ __global__ void __launch_bounds__(kSumThreads, 4) k_embed_join(
 }
 
 struct GradWork {
-  long long sortBytes, partBytes;
+  long long sortBytes, partBytes, markBytes;  // (a mark for each chunk)
+  long long all() const { return sortBytes + partBytes + markBytes; }
 };
 GradWork grad_work(int vocab, int dim, int n) {
-  GradWork w{0, 0};
+  GradWork w{0, 0, 0};
   if (vocab <= 0 || dim <= 0 || n <= 0) return w;
   w.sortBytes = n <= kSortMost ? 2LL * n * (long long)sizeof(int)
                                : (long long)token_sort_scratch_bytes(n, vocab);
   w.sortBytes = (w.sortBytes + 255) & ~255LL;
   for (const int E : {8, 4}) {  // whichever the pointers will allow
-    const long long b = 2 * sum_shape(n, dim, E).chunks * (long long)dim * 4;
-    w.partBytes = b > w.partBytes ? b : w.partBytes;
+    const long long chunks = sum_shape(n, dim, E).chunks;
+    w.partBytes = std::max(w.partBytes, 2 * chunks * dim * 4);
+    w.markBytes = std::max(w.markBytes, chunks);
   }
   return w;
 }
@@ -737,7 +757,8 @@ cudaError_t launch_sort(int n, int vocab, const void* tokens, int wide, int bloc
 template <class T, class O, int E, bool ADD>
 cudaError_t launch_sums(const SumShape& shape, dim3 grid, int n, int vocab, int dim,
                         const SortedTokens& sorted, const T* g, long long ldg, float scale,
-                        O* dtable, long long ldd, float* part, cudaStream_t s) {
+                        O* dtable, long long ldd, float* part, unsigned char* goesOn,
+                        cudaStream_t s) {
   const auto sum = k_embed_sum<T, O, E == 1 ? 4 : E, E == 1, ADD>;
   constexpr int smem = E == 1 ? 0 : kSumSmem<T, O, E, ADD>;
   static KernelOnce once;
@@ -745,16 +766,18 @@ cudaError_t launch_sums(const SumShape& shape, dim3 grid, int n, int vocab, int 
   if (e != cudaSuccess) return e;
   e = launch_dependent_smem(sum, grid, kSumThreads, smem, s, n, vocab, dim, shape.G, shape.chunk,
                             shape.chunks, (unsigned)shape.blocksX, sorted, g, ldg, scale, dtable,
-                            ldd, part);
+                            ldd, part, goesOn);
   if (e != cudaSuccess || shape.chunks <= 2) return e;
-  const long long lanes = ((long long)dim + E - 1) / E;
+  constexpr int kJoinE = E < 4 ? E : 4;
+  const long long lanes = ((long long)dim + kJoinE - 1) / kJoinE;
   int logL = 0;
-  while (logL < 5 && (1 << logL) < lanes) ++logL;
-  return launch_dependent(k_embed_join<O, E, ADD>,
-                          dim3((unsigned)((shape.chunks + kJoinChunks - 1) / kJoinChunks),
+  while (logL < 6 && (1 << logL) < lanes) ++logL;
+  const long long looks = (shape.chunks + kJoinChunks - 1) / kJoinChunks;
+  return launch_dependent(k_embed_join<O, kJoinE, ADD>,
+                          dim3((unsigned)(looks * kJoinBlocks),
                                (unsigned)((lanes + (1 << logL) - 1) >> logL)),
-                          kSumThreads, s, n, vocab, dim, logL, shape.chunk, shape.chunks, sorted,
-                          (const float*)part, scale, dtable, ldd);
+                          kSumThreads, s, dim, logL, shape.chunk, shape.chunks, sorted,
+                          (const unsigned char*)goesOn, (const float*)part, scale, dtable, ldd);
 }
 
 }  // namespace
@@ -811,7 +834,7 @@ int spmv_embed(int32_t vocab, int32_t dim, spmv_dtype tableType, const void* d_t
 int spmv_embed_grad_workspace(int32_t vocab, int32_t dim, int32_t nTokens, int64_t* bytes) {
   if (vocab < 0 || dim < 0 || nTokens < 0 || !bytes) return SPMV_ERR_INVALID_ARG;
   const spmv::GradWork w = spmv::grad_work(vocab, dim, nTokens);
-  *bytes = w.sortBytes + w.partBytes;
+  *bytes = w.all();
   return SPMV_OK;
 }
 
@@ -828,7 +851,7 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
   if (vocab == 0 || dim == 0 || (nTokens == 0 && accumulate)) return SPMV_OK;
   const GradWork w = grad_work(vocab, dim, nTokens);
   if (!d_dtable || (nTokens > 0 && (!d_g || !d_tokens || !d_work))) return SPMV_ERR_INVALID_ARG;
-  if (nTokens > 0 && workBytes < w.sortBytes + w.partBytes) return SPMV_ERR_INVALID_ARG;
+  if (nTokens > 0 && workBytes < w.all()) return SPMV_ERR_INVALID_ARG;
   if (misaligned(d_g, dtype_bytes(gType)) || misaligned(d_dtable, dtype_bytes(tableType)) ||
       misaligned(d_tokens, indexBytes) || (nTokens > 0 && misaligned(d_work, 16)))
     return SPMV_ERR_INVALID_ARG;
@@ -845,6 +868,7 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
   if (st != SPMV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* part = reinterpret_cast<float*>(static_cast<char*>(d_work) + w.sortBytes);
+  unsigned char* goesOn = static_cast<unsigned char*>(d_work) + w.sortBytes + w.partBytes;
   SortedTokens sorted{nullptr, nullptr, 1};
   if (nTokens > kSortMost) {
     st = record_cuda(launch_token_sort(nTokens, vocab, d_tokens, indexBytes, d_work, &sorted.pos,
@@ -876,8 +900,8 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
   const SumShape shape = sum_shape(nTokens, dim, std::max(E, 4));
   const long long zeroBlocks = accumulate ? 0 : ((long long)vocab + kZeroRows - 1) / kZeroRows;
   const dim3 grid((unsigned)(shape.blocksX + zeroBlocks), (unsigned)shape.slabs);
-  // (the second kernel's slabs are of 32 lanes)
-  if (((long long)dim + 32 * E - 1) / (32 * E) > 65535 ||
+  // (the second kernel's slabs are of 64 lanes with 4 columns at most)
+  if (((long long)dim + 63) / 64 > 65535 ||
       shape.blocksX + zeroBlocks > 0x7fffffffLL)
     return SPMV_ERR_TOO_LARGE;
   return record_cuda(with_dtype(gType, [&](auto gv) {
@@ -893,7 +917,7 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
                                                    : launch_sums<T, O, 1, false>);
       return launch(shape, grid, (int)nTokens, (int)vocab, (int)dim, sorted,
                     static_cast<const T*>(d_g), (long long)ld_g, scale,
-                    static_cast<O*>(d_dtable), (long long)ld_dtable, part, s);
+                    static_cast<O*>(d_dtable), (long long)ld_dtable, part, goesOn, s);
     });
   }));
 }
