@@ -428,16 +428,19 @@ def spmv_embed_grad(g, tokens, dtable, scale=1.0, accumulate=False, workspace=No
     st = _stream_of(stream, dtable)
     if workspace is None:
         nbytes = spmv_embed_grad_workspace(vocab, dim, n)
-        # taken on the launching stream, so that torch reuses it only after the call's work
-        if stream is None or st == _stream_of(None, dtable):
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dtable.device)
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(st, dtable.device)):
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dtable.device)
-    _check(_lib.spmv_embed_grad(vocab, dim, _dtype(g, "g"), gp, ldg, n, size, kp, scale,
-                                1 if accumulate else 0, _dtype(dtable, "dtable"), dp, ldd,
-                                _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                st), "spmv_embed_grad")
+        # from torch's allocator, for the launching stream, so that torch hands it out
+        # again only behind the call's work there (as a tensor it cost 7 us more, of 12)
+        wp = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, st) if nbytes else None
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+        wp = _ptr(workspace)
+    try:
+        _check(_lib.spmv_embed_grad(vocab, dim, _dtype(g, "g"), gp, ldg, n, size, kp, scale,
+                                    1 if accumulate else 0, _dtype(dtable, "dtable"), dp, ldd,
+                                    wp, nbytes, st), "spmv_embed_grad")
+    finally:
+        if workspace is None and wp:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(wp)
 
 
 def spmv_status_string(code):
