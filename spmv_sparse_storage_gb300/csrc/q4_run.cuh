@@ -295,8 +295,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_q4_run(const RunArgs p) {
   // other forms lose by it)
   constexpr int kSet = NT == 1 || kParts > 1 || !ALIGNED ? 1 : 4;
   const int sets = kSet == 1 ? p.n : (p.n + kSet - 1) / kSet;
+  // (rounded up without passing 32 bits at the largest column counts)
   const int rowBytes = a.cols / 2 + a.cols % 2;
-  const int groups = (a.cols + G - 1) / G;
+  const int groups = a.cols / G + (a.cols % G != 0);
   const X* x = static_cast<const X*>(p.x);
   const int scaleBytes = a.scale_type == SPMV_F32 ? 4 : 2;
   const int scaleShift = a.scale_type == SPMV_BF16 ? 16 : 0;

@@ -378,6 +378,33 @@ def test_offsets_past_32_bits(sp):
     assert np.array_equal(host(out), values[[39, 0]].astype(np.float32))
 
 
+@pytest.mark.parametrize("group", [32, 128])
+def test_the_widest_row(sp, group):
+    """As many columns as an int32 holds, in 1 GB of codes, with results from the columns
+    at the two ends. The columns between have the value 0, so that their terms are exact
+    and the bound is that of the few groups at the ends."""
+    cols = 2 ** 31 - 1
+    groups, tail = -(-cols // group), (cols // group - 2) * group
+    codes = torch.full((1, (cols + 1) // 2), 0x88, dtype=torch.uint8, device="cuda")
+    scales = torch.ones(1, groups, dtype=torch.bfloat16, device="cuda")
+    x = torch.ones(1, cols, dtype=torch.bfloat16, device="cuda")
+    want, mag = np.zeros((1, 1)), np.zeros((1, 1))
+    for seed, first in ((21, 0), (22, tail)):
+        n = min(3 * group, cols - first)
+        part, part_scales, _ = make(seed, 1, n, group, "bf16", False)
+        v = ot.round_to(np.random.default_rng(seed).standard_normal((1, n)), "bf16")
+        codes[:, first // 2:first // 2 + part.shape[1]] = dev(part)
+        scales[:, first // group:first // group + part_scales.shape[1]] = dev(part_scales, "bf16")
+        x[:, first:first + n] = dev(v, "bf16")
+        y, m = ot.q4_run(ot.q4_values(part, part_scales, None, group, n), v)
+        want, mag = want + y, mag + m
+    y = torch.full((1, 1), 7.0, device="cuda")
+    sp.spmv_q4_run(codes, scales, group, x, y)
+    bound = (8 + 6 + 32) * 2.0 ** -22 * mag + ot.half_ulp(np.abs(want), "f32")
+    assert abs(host(y)[0, 0] - want[0, 0]) <= bound[0, 0]
+    assert abs(want[0, 0]) > 100 * bound[0, 0]  # y = 0 fails
+
+
 # --- refusals ----------------------------------------------------------------------------------
 def test_refusals(sp):
     import ctypes as C
