@@ -415,9 +415,10 @@ int spmv_q4_quantize(const spmv_q4 *a, spmv_dtype wType, const void *d_w, int64_
  *   (SPMV_ERR_INVALID_ARG). xType and yType are independent.
  * Products are exact and summed in fp32, a group's sum times its scale, so
  * sum over a group of |code - zero| |x| has to stay within fp32. Per entry the
- * result is within (40 + ceil(cols / group)) * 2^-22 * (sum_k |A[r][k] x[k]| +
- * |c|) of the exact value before the rounding to yType. Asynchronous. The
- * matrix is read once for every 16 vectors (5 of fp32). */
+ * result is within (40 + ceil(cols / group)) * (2^-22 * (sum_k |A[r][k] x[k]| +
+ * |c|) + 2^-148) of the exact value before the rounding to yType (the last term
+ * for sums among fp32's subnormal numbers; vectors of any finite size count in
+ * full). Asynchronous. The matrix is read once for every 16 vectors (5 of fp32). */
 int spmv_q4_run(const spmv_q4 *a, int32_t n, spmv_dtype xType, const void *d_x, int64_t ldx,
                 const void *d_c, int64_t ldc, spmv_dtype yType, void *d_y, int64_t ldy,
                 void *stream);

@@ -5,9 +5,11 @@
 // exact in 16 bits and so are the vectors there: the group sums are products of
 // small matrices with exact operands and fp32 accumulators, which
 // mma.sync.m16n8k16 forms 16 rows and 8 columns at a time. An fp32 x is cut
-// into three bf16 parts that add up to it bit for bit (8 + 8 + 8 significant
-// bits, by truncation), each a column of its own; their sums are added at the
-// end.
+// into three bf16 parts, each a column of its own: x = p1 + 2^-7 p2 + 2^-16 p3
+// bit for bit, with p1 by truncation, p2 to nearest and p3 what is left (8
+// bits). Held so much larger than what they stand for, p2 and p3 lose nothing to
+// bf16's least number (2^-133) even of a subnormal x, and no part is larger than
+// |x| or 2^-125; their sums are added with these weights at the end.
 //
 // What bounds it: with 1 to 8 columns the bytes of A, half a byte per entry and one
 // scale per group, read once for up to 16 columns, and close behind the
@@ -186,7 +188,7 @@ __device__ __forceinline__ uint4 in_operand_order(const unsigned (&h)[8]) {
   return make_uint4(h[0] | h[4] << 16, h[1] | h[5] << 16, h[2] | h[6] << 16, h[3] | h[7] << 16);
 }
 // Their 16-bit operands in the order 0 4 1 5 2 6 3 7; an fp32 vector's three
-// parts go to three columns (4 pieces apart).
+// parts (p1, p2, p3 above) go to three columns (4 pieces apart).
 template <class X>
 __device__ __forceinline__ void stage_x(const Pack<X, 8>& v, uint4* out) {
   unsigned h[8];
@@ -197,25 +199,33 @@ __device__ __forceinline__ void stage_x(const Pack<X, 8>& v, uint4* out) {
 template <>
 __device__ __forceinline__ void stage_x<float>(const Pack<float, 8>& in, uint4* out) {
   float v[8];
+  unsigned h[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = in.v[i];
-#pragma unroll
-  for (int p = 0; p < 3; ++p) {
-    unsigned h[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const unsigned bits = __float_as_uint(v[i]);
-      if ((bits & 0x7f800000u) == 0x7f800000u) {
-        // an infinity or a NaN is its first part alone (a NaN kept one by a bit)
-        h[i] = (bits >> 16) | ((bits & 0x007fffffu) ? 0x40u : 0u);
-        v[i] = 0.0f;
-      } else {
-        h[i] = bits >> 16;
-        v[i] -= __uint_as_float(bits & 0xffff0000u);
-      }
+  for (int i = 0; i < 8; ++i) {
+    const unsigned bits = __float_as_uint(in.v[i]);
+    h[i] = bits >> 16;
+    if ((bits & 0x7f800000u) == 0x7f800000u) {
+      // an infinity or a NaN is its first part alone (a NaN kept one by a bit)
+      h[i] |= (bits & 0x007fffffu) ? 0x40u : 0u;
+      v[i] = 0.0f;
+    } else {
+      v[i] = (in.v[i] - __uint_as_float(bits & 0xffff0000u)) * 128.0f;
     }
-    out[p * 4] = in_operand_order(h);
   }
+  out[0] = in_operand_order(h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    h[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+    v[i] = (v[i] - __uint_as_float(h[i] << 16)) * 512.0f;
+  }
+  out[4] = in_operand_order(h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = __float_as_uint(v[i]) >> 16;  // (the lower half is 0)
+  out[8] = in_operand_order(h);
+}
+// What a part's sums count for.
+__device__ __forceinline__ constexpr float part_weight(int q) {
+  return q == 0 ? 1.0f : q == 1 ? 1.0f / 128.0f : 1.0f / 65536.0f;
 }
 
 // A scale from its bits: fp32 (shift 0), bf16 (shift 16) or fp16.
@@ -644,8 +654,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_q4_run(const RunArgs p) {
         for (int b = 0; b < kSet; ++b)
           if (v0 + b < p.n)
 #pragma unroll
-            for (int q = 0; q < kParts; ++q)
-              sum[b] += in[(size_t)w * slotFloats + (b * kParts + q) * kTileRows];
+            for (int q = kParts - 1; q >= 0; --q)  // (p1 + p2 may overflow where x does not)
+              sum[b] = fmaf(in[(size_t)w * slotFloats + (b * kParts + q) * kTileRows],
+                            part_weight(q), sum[b]);
       };
       if (units >= kWarps) {
 #pragma unroll 4

@@ -405,6 +405,41 @@ def test_the_widest_row(sp, group):
     assert abs(want[0, 0]) > 100 * bound[0, 0]  # y = 0 fails
 
 
+def test_fp32_vectors_come_back_bit_for_bit(sp):
+    """The unit matrix times vectors of every finite exponent, subnormal ones among them."""
+    rng = np.random.default_rng(17)
+    bits = rng.integers(0, 2 ** 32, (70, 32), dtype=np.uint64).astype(np.uint32)
+    bits[:10] &= 0x807FFFFF  # subnormal
+    bits[10:30] = (bits[10:30] & 0x807FFFFF) | (rng.integers(1, 24, (20, 32)) << 23).astype(
+        np.uint32)
+    bits[30, :5] = [0, 0x80000000, 1, 0x7F7FFFFF, 0x00800000]
+    x = bits.view(np.float32)
+    x[~np.isfinite(x)] = 1.5
+    codes = ot.pack(np.full((32, 32), 8, np.uint8) + np.eye(32, dtype=np.uint8))
+    y = torch.empty(70, 32, device="cuda")
+    sp.spmv_q4_run(dev(codes), torch.ones(32, 1, device="cuda"), 32, dev(x), y)
+    assert np.array_equal(host(y), x)
+
+
+@pytest.mark.parametrize("x_type,scale", [("f32", 1e-36), ("f32", 1e-37), ("f32", 1e-38),
+                                          ("f32", 1e-40), ("f32", 1e-42), ("bf16", 1e-37),
+                                          ("bf16", 1e-39)])
+def test_tiny_vectors(sp, x_type, scale):
+    """Within the stated bound, whose absolute term (a rounding to a multiple of 2^-149 for
+    each group's sum and each partial sum's three parts) is far below the results."""
+    rows, cols, group = 40, 333, 32
+    codes, scales, z = make(15, rows, cols, group, "f32", True)
+    scales *= 50
+    x = ot.round_to((np.random.default_rng(16).standard_normal((3, cols)) * scale)
+                    .astype(np.float32), x_type)
+    want, mag = ot.q4_run(ot.q4_values(codes, scales, z, group, cols), x)
+    y = torch.zeros(3, rows, device="cuda")
+    sp.spmv_q4_run(dev(codes), dev(scales), group, dev(x, x_type), y, zeros=dev(z))
+    bound = (40 + scales.shape[1]) * (2.0 ** -22 * mag + 2.0 ** -148)
+    assert np.all(np.abs(host(y).astype(np.float64) - want) <= bound)
+    assert np.all(bound < mag / 50) and np.mean(np.abs(want) > bound) > 0.9  # y = 0 fails
+
+
 # --- refusals ----------------------------------------------------------------------------------
 def test_refusals(sp):
     import ctypes as C
