@@ -332,17 +332,20 @@ def _tokens(t):
 
 
 def _q4_view(codes, scales, group, cols, zeros):
-    """The spmv_q4 of the arrays (which the caller keeps alive)."""
+    """The spmv_q4 of the arrays (which the caller keeps alive): codes of
+    ceil(cols/2) bytes and ceil(cols/group) scales and zero points to a row."""
     cp, rows, width, ldc = _matrix(codes, "codes", torch.uint8)
     sp_, srows, swidth, lds = _matrix(scales, "scales")
-    groups = -(-cols // group) if group in (32, 64, 128) else 0  # else the library refuses
-    if srows != rows or swidth < groups or width < (cols + 1) // 2:
+    # (wider arrays are those of another matrix: rows with padding are views; a group
+    # that there is not is left for the library to refuse)
+    groups = -(-cols // group) if group in (32, 64, 128) else swidth
+    if srows != rows or swidth != groups or width != (cols + 1) // 2:
         raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not "
                          f"hold {cols} columns in groups of {group}")
     zp, ldz = None, 0
     if zeros is not None:
         zp, zrows, zwidth, ldz = _matrix(zeros, "zeros", torch.uint8)
-        if zrows != rows or zwidth < groups:
+        if zrows != rows or zwidth != groups:
             raise ValueError(f"zeros {tuple(zeros.shape)} do not match scales "
                              f"{tuple(scales.shape)}")
     return spmv_q4(rows, cols, group, _dtype(scales, "scales"), cp, ldc, sp_, lds, zp, ldz)

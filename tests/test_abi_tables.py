@@ -145,3 +145,31 @@ def test_binding_refuses_host_tensors_and_wrong_types(sp):
         sp.spmv_q4_quantize(t, t, t, 32)
     with pytest.raises(ValueError):
         sp.spmv_embed_grad(t, torch.zeros(4, dtype=torch.int64), t)
+
+
+class OnDevice:
+    """What the binding looks at of a contiguous CUDA tensor."""
+    is_cuda = True
+
+    def __init__(self, rows, cols, dtype=torch.float32):
+        self.shape, self.dtype = (rows, cols), dtype
+
+    def stride(self):
+        return self.shape[1], 1
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+@pytest.mark.parametrize("codes,scales,zeros", [(64, 4, 4), (32, 4, 2), (64, 2, 2), (32, 2, 4),
+                                                (31, 2, 2), (32, 1, 2), (33, 2, 2)])
+def test_binding_refuses_a_matrix_of_another_width(sp, codes, scales, zeros):
+    """Codes, scales or zero points of more or fewer columns than the vectors, the
+    results or the dense matrix have (64)."""
+    c, s = OnDevice(4, codes, torch.uint8), OnDevice(4, scales)
+    z = OnDevice(4, zeros, torch.uint8)
+    for call in (lambda: sp.spmv_q4_run(c, s, 32, OnDevice(1, 64), OnDevice(1, 4), zeros=z),
+                 lambda: sp.spmv_q4_quantize(OnDevice(4, 64), c, s, 32, zeros=z),
+                 lambda: sp.spmv_embed_q4(c, s, 32, None, OnDevice(4, 64), zeros=z)):
+        with pytest.raises(ValueError):
+            call()
