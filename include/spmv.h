@@ -450,7 +450,8 @@ int spmv_embed_q4(const spmv_q4 *a, int32_t nTokens, int32_t indexBytes, const v
  *   d_work: scratch of at least spmv_embed_grad_workspace(...) bytes, 16-byte
  *   aligned, free again when the call's work on `stream` is done
  *   (SPMV_ERR_INVALID_ARG when smaller; may be NULL when that is 0).
- * g, dtable and d_work may not overlap. Asynchronous. */
+ * g, dtable and d_work may not overlap. dim is at most 64 * 65535
+ * (SPMV_ERR_TOO_LARGE, before any work). Asynchronous. */
 int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void *d_g, int64_t ld_g,
                     int32_t nTokens, int32_t indexBytes, const void *d_tokens, float scale,
                     int32_t accumulate, spmv_dtype tableType, void *d_dtable, int64_t ld_dtable,

@@ -863,6 +863,15 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
       overlap(d_tokens, (long long)nTokens * indexBytes, d_dtable, tBytes) ||
       overlap(d_tokens, (long long)nTokens * indexBytes, d_work, wBytes))
     return SPMV_ERR_INVALID_ARG;
+  const int gb = dtype_bytes(gType), tb = dtype_bytes(tableType);
+  const int most = sum_most(gb, tb);
+  const int E = std::min(elements_at_once(d_g, ld_g, dim, gb, most),
+                         elements_at_once(d_dtable, ld_dtable, dim, tb, most));
+  const SumShape shape = sum_shape(nTokens, dim, std::max(E, 4));
+  const long long zeroBlocks = accumulate ? 0 : ((long long)vocab + kZeroRows - 1) / kZeroRows;
+  // (the second kernel's slabs are of 64 lanes with 4 columns at most)
+  if (((long long)dim + 63) / 64 > 65535 || shape.blocksX + zeroBlocks > 0x7fffffffLL)
+    return SPMV_ERR_TOO_LARGE;
   const void* ptrs[] = {d_g, d_tokens, d_dtable, d_work};
   int st = check_current_device_ptrs(ptrs, nTokens > 0 ? 4 : 3);
   if (st != SPMV_OK) return st;
@@ -893,17 +902,7 @@ int spmv_embed_grad(int32_t vocab, int32_t dim, spmv_dtype gType, const void* d_
     sorted = {&out->x, &out->y, 2};
   }
   if (st != SPMV_OK) return st;
-  const int gb = dtype_bytes(gType), tb = dtype_bytes(tableType);
-  const int most = sum_most(gb, tb);
-  const int E = std::min(elements_at_once(d_g, ld_g, dim, gb, most),
-                         elements_at_once(d_dtable, ld_dtable, dim, tb, most));
-  const SumShape shape = sum_shape(nTokens, dim, std::max(E, 4));
-  const long long zeroBlocks = accumulate ? 0 : ((long long)vocab + kZeroRows - 1) / kZeroRows;
   const dim3 grid((unsigned)(shape.blocksX + zeroBlocks), (unsigned)shape.slabs);
-  // (the second kernel's slabs are of 64 lanes with 4 columns at most)
-  if (((long long)dim + 63) / 64 > 65535 ||
-      shape.blocksX + zeroBlocks > 0x7fffffffLL)
-    return SPMV_ERR_TOO_LARGE;
   return record_cuda(with_dtype(gType, [&](auto gv) {
     return with_dtype(tableType, [&](auto ov) {
       using T = decltype(gv);

@@ -173,3 +173,12 @@ def test_binding_refuses_a_matrix_of_another_width(sp, codes, scales, zeros):
                  lambda: sp.spmv_embed_q4(c, s, 32, None, OnDevice(4, 64), zeros=z)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_gradients_that_are_too_wide_are_refused_before_any_work(sp):
+    """Before the sort's launch, so before the pointers are even looked up."""
+    p, dim = 1 << 40, 64 * 65535 + 1
+    call = lambda d: sp._lib.spmv_embed_grad(  # noqa: E731
+        10, d, 0, p, d, 4, 4, 2 * p, 1.0, 0, 0, 3 * p, d, 4 * p, 1 << 35, None)
+    assert call(dim) == sp.SPMV_ERR_TOO_LARGE
+    assert call(dim - 1) != sp.SPMV_ERR_TOO_LARGE
