@@ -279,8 +279,27 @@ def spmv_run_csr_noalloc(num_rows, num_cols, nnz, row_ptrs, col_idx, value, x, y
 
 # --- dense tables: 4-bit matrices and token lookups --------------------------------
 # The handle of a device's current stream. torch.cuda.current_stream builds an
-# object for it, 2.8 us of a call that takes the GPU 4.
+# object for it, 2.8 us of a call that takes the GPU 4. Memory from torch's allocator
+# for a stream, and back: the same by the calls below torch's own (a tensor instead
+# cost 7 us more, of 12). Where this torch lacks them, its public ones serve.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+
+
+def _take_scratch(nbytes, stream):
+    """nbytes of the current device for work on ``stream`` (a handle): torch hands
+    memory that is freed out again only behind what that stream was given before."""
+    if _raw_alloc is not None and _raw_free is not None:
+        return _raw_alloc(nbytes, stream)
+    return torch.cuda.caching_allocator_alloc(nbytes, stream=stream)
+
+
+def _free_scratch(p):
+    if _raw_alloc is not None and _raw_free is not None:
+        _raw_free(p)
+    else:
+        torch.cuda.caching_allocator_delete(p)
 
 
 def _stream_of(stream, t):
@@ -431,9 +450,7 @@ def spmv_embed_grad(g, tokens, dtable, scale=1.0, accumulate=False, workspace=No
     st = _stream_of(stream, dtable)
     if workspace is None:
         nbytes = spmv_embed_grad_workspace(vocab, dim, n)
-        # from torch's allocator, for the launching stream, so that torch hands it out
-        # again only behind the call's work there (as a tensor it cost 7 us more, of 12)
-        wp = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, st) if nbytes else None
+        wp = _take_scratch(nbytes, st) if nbytes else None
     else:
         nbytes = workspace.numel() * workspace.element_size()
         wp = _ptr(workspace)
@@ -443,7 +460,7 @@ def spmv_embed_grad(g, tokens, dtable, scale=1.0, accumulate=False, workspace=No
                                     wp, nbytes, st), "spmv_embed_grad")
     finally:
         if workspace is None and wp:
-            torch._C._cuda_cudaCachingAllocator_raw_delete(wp)
+            _free_scratch(wp)
 
 
 def spmv_status_string(code):

@@ -317,6 +317,71 @@ def test_lookup_and_gradient_on_another_stream_and_in_a_graph(sp):
         assert torch.equal(out, first[dk])
 
 
+@pytest.fixture(params=["direct", "public"])
+def scratch(request, sp, monkeypatch):
+    """Scratch by either way of asking torch for it."""
+    if request.param == "public":
+        monkeypatch.setattr(sp, "_raw_alloc", None)
+        monkeypatch.setattr(sp, "_raw_free", None)
+
+
+def test_scratch_of_its_own_in_a_graph(sp, scratch):
+    """Two gradients captured with no workspace given; what is allocated and written
+    between the replays reaches neither."""
+    rng = np.random.default_rng(3)
+    n, vocab, dim = 3000, 400, 64
+    tokens = rng.integers(-1, vocab, n)
+    dg, dk = dev(rng.standard_normal((n, dim)).astype(np.float32)), dev(tokens)
+    one, two = torch.empty(vocab, dim, device="cuda"), torch.empty(vocab, dim, device="cuda")
+    sp.spmv_embed_grad(dg, dk, one)
+    check_grad(host(one), host(dg), tokens, vocab, 1.0, "f32")
+    want = one.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sp.spmv_embed_grad(dg, dk, one)
+        sp.spmv_embed_grad(dg, dk, two, scale=2.0)
+    size = sp.spmv_embed_grad_workspace(vocab, dim, n)
+    for _ in range(3):
+        one.zero_()
+        two.zero_()
+        other = [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        graph.replay()
+        other += [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert torch.equal(one, want) and torch.equal(two, 2 * want)
+
+
+def test_scratch_of_its_own_beside_other_work(sp, scratch):
+    """Gradients on a stream that is behind (a large product is ahead of them there),
+    while another stream takes memory of the scratch's size and writes it."""
+    rng = np.random.default_rng(4)
+    n, vocab, dim = 5000, 300, 64
+    tokens = rng.integers(-1, vocab, n)
+    dg, dk = dev(rng.standard_normal((n, dim)).astype(np.float32)), dev(tokens)
+    outs = [torch.empty(vocab, dim, device="cuda") for _ in range(4)]
+    sp.spmv_embed_grad(dg, dk, outs[0])
+    check_grad(host(outs[0]), host(dg), tokens, vocab, 1.0, "f32")
+    want = outs[0].clone()
+    size = sp.spmv_embed_grad_workspace(vocab, dim, n)
+    a = torch.ones(4096, 4096, device="cuda")
+    b = torch.empty_like(a)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.mm(a, a, out=b)
+        for i, o in enumerate(outs):
+            if i % 2:
+                sp.spmv_embed_grad(dg, dk, o, stream=side)
+            else:
+                with torch.cuda.stream(side):
+                    sp.spmv_embed_grad(dg, dk, o)
+            torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
+
+
 def test_offsets_past_32_bits(sp):
     """A table of more than 2^31 elements: lookups from and gradients into its
     last rows."""
