@@ -423,9 +423,9 @@ __device__ __forceinline__ Pack<O, E> finished(const float (&acc)[E], float scal
 // of the row that begins in it. Blocks from sumBlocks on (in the first slab) zero
 // rows. The keys and places of a block's chunks, and the keys around them, wait in
 // shared memory, so that only the rows of g (and those added to) are waited for.
-// A thread's share of a row (8 to 32 bytes, E = 8 or 4) is fetched kAhead rows ahead
-// by asynchronous copies into its own place in shared memory, which takes no
-// registers and no barrier. Rows of any alignment (APART) come by single elements, 4
+// A thread's share of a row (8 or 16 bytes, E = 8 or 4) is fetched 7 rows ahead, by
+// asynchronous copies into its own places in shared memory (kSlots of them), which
+// takes no registers and no barrier. Rows of any alignment (APART) come by single elements, 4
 // to a thread as far apart as the threads of its group, R rows at a time into
 // registers (16384 tokens of 4099 bf16 columns 152 us; one element to a thread, four
 // times the groups, 200; loads under conditions 231). (4 rows
@@ -439,38 +439,25 @@ __device__ __forceinline__ Pack<O, E> finished(const float (&acc)[E], float scal
 constexpr int sum_most(int gBytes, int tableBytes) {
   return gBytes == 2 && tableBytes == 2 ? 8 : 4;
 }
+constexpr int kSlots = 8;
 template <class T, class O, int E, bool ADD>
 constexpr int kSlotBytes = E * (int)(sizeof(T) + (ADD ? sizeof(O) : 0));
 template <class T, class O, int E, bool ADD>
-constexpr int kAhead = kSlotBytes<T, O, E, ADD> > 32 ? 4 : 8;
-template <class T, class O, int E, bool ADD>
-constexpr int kSumSmem =
-    kAhead<T, O, E, ADD> * kSumThreads * kSlotBytes<T, O, E, ADD>;
-// BYTES of this thread in pieces of 16 (or 8) bytes, each kind of piece of all
-// threads together (no bank conflicts): to shared memory and from there.
+constexpr int kSumSmem = kSlots * kSumThreads * kSlotBytes<T, O, E, ADD>;
+// A thread's share, to shared memory and from there.
 template <int BYTES>
 __device__ __forceinline__ void fetch_share(unsigned char* all, const void* gmem) {
-  constexpr int P = BYTES < 16 ? BYTES : 16;
-#pragma unroll
-  for (int q = 0; q < BYTES / P; ++q) {
-    unsigned char* const to = all + (q * kSumThreads + threadIdx.x) * P;
-    const unsigned char* const from = static_cast<const unsigned char*>(gmem) + P * q;
-    if constexpr (P == 16)
-      cp_async16(to, from);
-    else
-      cp_async_small<P>(to, from);
-  }
+  static_assert(BYTES == 8 || BYTES == 16, "one access");
+  unsigned char* const to = all + threadIdx.x * BYTES;
+  if constexpr (BYTES == 16)
+    cp_async16(to, gmem);
+  else
+    cp_async_small<BYTES>(to, gmem);
 }
 template <class V>
 __device__ __forceinline__ V own_share(const unsigned char* all) {
-  constexpr int BYTES = (int)sizeof(V), P = BYTES < 16 ? BYTES : 16;
-  using Piece = Pack<unsigned, P / 4>;
-  V v;
-#pragma unroll
-  for (int q = 0; q < BYTES / P; ++q)
-    reinterpret_cast<Piece*>(&v)[q] =
-        *reinterpret_cast<const Piece*>(all + (q * kSumThreads + threadIdx.x) * P);
-  return v;
+  static_assert(sizeof(V) == 8 || sizeof(V) == 16, "one access");
+  return reinterpret_cast<const V*>(all)[threadIdx.x];
 }
 
 template <class T, class O, int E, bool APART, bool ADD>
@@ -566,7 +553,7 @@ __global__ void __launch_bounds__(kSumThreads, 3) k_embed_sum(
     }
   };
   if constexpr (!APART) {
-    constexpr int kD = kAhead<T, O, E, ADD>, kT = E * (int)sizeof(T), kO = E * (int)sizeof(O);
+    constexpr int kD = kSlots, kT = E * (int)sizeof(T), kO = E * (int)sizeof(O);
     // slot j: every thread's share of a row of g, then of the row added to
     auto slot = [&](int j) { return ring + (size_t)j * kSumThreads * kSlotBytes<T, O, E, ADD>; };
     int next = begin;  // the next position to fetch
