@@ -279,27 +279,23 @@ def spmv_run_csr_noalloc(num_rows, num_cols, nnz, row_ptrs, col_idx, value, x, y
 
 # --- dense tables: 4-bit matrices and token lookups --------------------------------
 # The handle of a device's current stream. torch.cuda.current_stream builds an
-# object for it, 2.8 us of a call that takes the GPU 4. Memory from torch's allocator
-# for a stream, and back: the same by the calls below torch's own (a tensor instead
-# cost 7 us more, of 12). Where this torch lacks them, its public ones serve.
+# object for it, 2.8 us of a call that takes the GPU 4.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
-_raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
 
 
-def _take_scratch(nbytes, stream):
-    """nbytes of the current device for work on ``stream`` (a handle): torch hands
-    memory that is freed out again only behind what that stream was given before."""
-    if _raw_alloc is not None and _raw_free is not None:
-        return _raw_alloc(nbytes, stream)
+# Memory of the current device for work on a stream (its handle), from torch's
+# allocator, which hands out again what is freed only behind what that stream was given
+# before; and the way back. By the calls below torch's public ones, where this torch has
+# them: a tensor instead cost 7 us more, of 12, and one more Python call each about 1.
+def _public_take(nbytes, stream):
     return torch.cuda.caching_allocator_alloc(nbytes, stream=stream)
 
 
-def _free_scratch(p):
-    if _raw_alloc is not None and _raw_free is not None:
-        _raw_free(p)
-    else:
-        torch.cuda.caching_allocator_delete(p)
+_public_free = torch.cuda.caching_allocator_delete
+_take_scratch = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_free_scratch = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+if _take_scratch is None or _free_scratch is None:
+    _take_scratch, _free_scratch = _public_take, _public_free
 
 
 def _stream_of(stream, t):

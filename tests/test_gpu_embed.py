@@ -321,8 +321,8 @@ def test_lookup_and_gradient_on_another_stream_and_in_a_graph(sp):
 def scratch(request, sp, monkeypatch):
     """Scratch by either way of asking torch for it."""
     if request.param == "public":
-        monkeypatch.setattr(sp, "_raw_alloc", None)
-        monkeypatch.setattr(sp, "_raw_free", None)
+        monkeypatch.setattr(sp, "_take_scratch", sp._public_take)
+        monkeypatch.setattr(sp, "_free_scratch", sp._public_free)
 
 
 def test_scratch_of_its_own_in_a_graph(sp, scratch):
