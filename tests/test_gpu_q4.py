@@ -325,6 +325,63 @@ def test_conversion_lookup_and_product_agree(sp):
     assert torch.equal(y.t(), back)
 
 
+# Products whose vectors a block takes into shared memory in several phases: (rows, columns,
+# vectors, their type, group, zero points, bytes of padding to a row of codes, whether c is
+# given, then the blocks that share a tile's columns; test_q4_plan.py asks for these and for
+# the phases). With 8 blocks and 32 * 8 x more bytes than a block has they have no choice;
+# the tall ones have several tiles to a block and more tiles than blocks.
+PHASED = [(32, 200_000, 16, "bf16", 128, False, 0, False, 8),
+          (32, 200_001, 16, "f16", 32, True, 0, True, 8),
+          (2600, 80_003, 4, "f32", 64, True, 0, True, 8),
+          (2600, 80_003, 4, "f32", 64, False, 14, False, 8),
+          (80_327, 5880, 5, "f32", 128, False, 4, True, 2),
+          (5647, 15_741, 16, "f16", 32, True, 0, False, 8),
+          (124_910, 4029, 5, "f32", 32, True, 1, True, 1),
+          (71_998, 1826, 16, "bf16", 64, True, 0, True, 1),
+          (163_092, 2622, 13, "bf16", 128, False, 0, False, 1)]
+
+
+def whole_product(codes, scales, zeros, group, x, c):
+    """(y, sum of magnitudes) in 64 bits on the GPU, a block of rows at a time."""
+    cols = x.shape[1]
+    k = torch.arange(cols, device="cuda")
+    xd = x.double()
+    ys, mags = [], []
+    for b in torch.arange(codes.shape[0], device="cuda").split(max(1, 2 ** 26 // cols)):
+        q = codes[b][:, k // 2]
+        a = torch.where(k % 2 == 0, q & 15, q >> 4).double()
+        a -= 8.0 if zeros is None else zeros[b][:, k // group].double()
+        a *= scales[b][:, k // group].double()
+        ys.append(xd @ a.t())
+        mags.append(xd.abs() @ a.abs().t())
+    y, mag = torch.cat(ys, 1), torch.cat(mags, 1)
+    return (y, mag) if c is None else (y + c.double(), mag + c.double().abs())
+
+
+@pytest.mark.parametrize("rows,cols,n,x_type,group,zeros,pad,residual,blocks", PHASED)
+def test_vectors_in_several_phases(sp, rows, cols, n, x_type, group, zeros, pad, residual,
+                                   blocks):
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols)
+    width, groups = (cols + 1) // 2, -(-cols // group)
+    codes = torch.randint(0, 256, (rows, width + pad), device="cuda", generator=gen,
+                          dtype=torch.uint8)[:, :width]
+    scales = torch.rand(rows, groups, device="cuda", generator=gen).sub_(0.5).mul_(0.04)
+    scales = scales.to(torch.bfloat16)
+    z = (torch.randint(0, 16, (rows, groups), device="cuda", generator=gen, dtype=torch.uint8)
+         if zeros else None)
+    x = torch.randn(n, cols, device="cuda", generator=gen).to(TYPES[x_type])
+    c = torch.randn(n, rows, device="cuda", generator=gen) if residual else None
+    y = torch.full((n, rows), float("nan"), device="cuda")
+    sp.spmv_q4_run(codes, scales, group, x, y, c=c, zeros=z)
+    want, mag = whole_product(codes, scales, z, group, x, c)
+    bound = (8 + groups + 32) * 2.0 ** -22 * mag
+    bound = bound + (want.abs() + bound) * 2.0 ** -24 + 2.0 ** -150  # half a unit of fp32
+    assert bool(((y.double() - want).abs() <= bound).all())
+    again = torch.zeros_like(y) if c is None else c.clone()
+    sp.spmv_q4_run(codes, scales, group, x, again, c=None if c is None else again, zeros=z)
+    assert torch.equal(again, y)  # bit for bit, and in place
+
+
 # --- streams, graphs, sizes ------------------------------------------------------------------
 def test_on_another_stream_and_in_a_graph(sp):
     codes, scales, z = make(12, 300, 1024, 64, "f16", True)
