@@ -286,6 +286,52 @@ def test_quantize_of_faulty_groups(sp, zeros, w_type, scale_type):
     assert np.all(np.isnan(got[fault])) and np.all(np.isfinite(got[~fault]))
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("w_type,scale_type", [("f32", "f32"), ("f32", "f16"), ("f16", "f16"),
+                                               ("f16", "f32"), ("bf16", "bf16"),
+                                               ("bf16", "f16")])
+@pytest.mark.parametrize("cols,group", [(256, 32), (331, 32), (1160, 64), (333, 128), (1, 32)])
+def test_quantize_of_faulty_groups_of_any_row(sp, cols, group, w_type, scale_type, zeros):
+    """Infinities and NaN at the first and the last column, in the middle and in a partial
+    last group, and scales that overflow or vanish, in rows of every alignment: exactly
+    their groups have values that are NaN, the others are converted as ever."""
+    large = {"f32": 3e38, "f16": 65504.0, "bf16": 3e38}[w_type]
+    least = {"f32": 1e-44, "f16": 2.0 ** -24, "bf16": 2.0 ** -133}[w_type]
+    rng = np.random.default_rng(cols)
+    w = rng.standard_normal((12, cols)).astype(np.float32)
+    w[0, 0] = np.inf
+    w[1, -1] = np.nan
+    w[2, cols // 2] = -np.inf
+    w[3] = np.nan
+    w[4, cols // 2] = large  # its scale overflows fp16 where the weight is of more range
+    w[5, cols // 2] = -large
+    w[6] = least  # a scale below the least of its type, or subnormal
+    w[7, ::3] = -large
+    w[7, 1::3] = large  # with zero points the range itself overflows fp32
+    w[8] = -least
+    w[9, cols // 2:] = 0
+    w[10, -1] = np.inf
+    w[10, 0] = np.nan
+    w = ot.round_to(w, w_type)
+    want_codes, want_scales, want_zeros = ot.q4_quantize(w, group, scale_type, zeros)
+    groups = want_scales.shape[1]
+    codes = torch.empty(12, (cols + 1) // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(12, groups, dtype=TYPES[scale_type], device="cuda")
+    z = torch.empty(12, groups, dtype=torch.uint8, device="cuda") if zeros else None
+    back = torch.empty(12, cols, dtype=TYPES[w_type], device="cuda")
+    sp.spmv_q4_quantize(dev(w, w_type), codes, scales, group, zeros=z, back=back)
+    assert np.array_equal(host(scales), want_scales, equal_nan=True)
+    assert np.array_equal(codes.cpu().numpy(), want_codes)
+    if zeros:
+        assert np.array_equal(z.cpu().numpy(), want_zeros)
+    fault = ~np.isfinite(want_scales).repeat(group, 1)[:, :cols]
+    got = host(back)
+    assert np.all(np.isnan(got[fault])) and not np.any(np.isnan(got[~fault]))
+    first, last = slice(0, group), slice((groups - 1) * group, cols)
+    assert np.all(fault[0, first]) and np.all(fault[1, last]) and np.all(fault[3])
+    assert not np.any(fault[0, group:]) and not np.any(fault[1, :(groups - 1) * group])
+
+
 # --- rows back in dense form -----------------------------------------------------------------
 @pytest.mark.parametrize("cols", [1, 31, 64, 100, 129, 1000, 4096])
 @pytest.mark.parametrize("group,scale_type,zeros,out_type", [
