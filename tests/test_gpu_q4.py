@@ -132,6 +132,32 @@ def test_accumulation_is_y_plus_ax(sp):
     check_product(host(y), values, x, y0, 2, "f32")
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 40), (70, 333), (33, 1024), (300, 96)])
+@pytest.mark.parametrize("x_type,y_type,per_pass", [("bf16", "f32", 16), ("f16", "f16", 16),
+                                                    ("f32", "f32", 5)])
+def test_many_vectors(sp, rows, cols, x_type, y_type, per_pass):
+    """A prompt's worth of vectors, at the numbers where another reading of the matrix
+    begins, in rows further apart than they are long: each the product that it is alone
+    or with the others of its reading, bit for bit, and nothing written between them."""
+    codes, scales, z = make(31, rows, cols, 32, "f16", True)
+    values = ot.q4_values(codes, scales, z, 32, cols)
+    dc, ds, dz = dev(codes), dev(scales, "f16"), dev(z)
+    rng = np.random.default_rng(rows)
+    for n in (per_pass, per_pass + 1, 4 * per_pass, 4 * per_pass + 1, 100, 257):
+        x = ot.round_to(rng.standard_normal((n, cols)), x_type)
+        c = ot.round_to(rng.standard_normal((n, rows)), y_type)
+        dx = padded(n, cols, TYPES[x_type], cols + 3, float("nan"))
+        dx.copy_(dev(x))
+        y = padded(n, rows, TYPES[y_type], rows + 5, 99.0)
+        sp.spmv_q4_run(dc, ds, 32, dx, y, c=dev(c, y_type), zeros=dz)
+        check_product(host(y), values, x, c, scales.shape[1], y_type)
+        assert torch.all(y._base[:, rows:] == 99.0)
+        first = n - 1 - (n - 1) % per_pass  # of the last reading
+        part = torch.empty(n - first, rows, dtype=TYPES[y_type], device="cuda")
+        sp.spmv_q4_run(dc, ds, 32, dx[first:], part, c=dev(c[first:], y_type), zeros=dz)
+        assert torch.equal(part, y[first:])
+
+
 @pytest.mark.parametrize("x_type", ["f32", "f16", "bf16"])
 def test_infinities_and_nan(sp, x_type):
     """An infinity or a NaN in x or in a scale reaches exactly the results
