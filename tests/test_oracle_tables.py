@@ -99,3 +99,25 @@ def test_embed_and_gradient_are_the_one_hot_products():
     base = rng.standard_normal((vocab, dim))
     added, _, _ = ot.embed_grad(g, tokens, vocab, 2.0, base)
     assert np.allclose(added, grad + base, rtol=0, atol=1e-14)
+
+
+@pytest.mark.parametrize("with_zeros,steps", [(False, 7), (True, 15)])
+def test_quantize_scale_against_fractions(with_zeros, steps):
+    """The factor is the fp32 number nearest to 1/7 or 1/15 and the scale is the range
+    times it, rounded once to fp32 and once to its type: within a unit of fp32 of the
+    range's exact quotient, as a division by a constant in fp32 is computed on a GPU."""
+    factor = Fraction(float(np.float32(1 / steps)))
+    near = [Fraction(float(np.nextafter(np.float32(1 / steps), np.float32(d)))) for d in (0, 1)]
+    assert all(abs(factor - Fraction(1, steps)) < abs(v - Fraction(1, steps)) for v in near)
+    rng = np.random.default_rng(12)
+    w = (rng.standard_normal((300, 32)) * 10.0 ** rng.integers(-20, 20, (300, 1))).astype(
+        np.float32)
+    for scale_type in ("f32", "bf16"):
+        _, scales, _ = ot.q4_quantize(w, 32, scale_type, with_zeros)
+        for row, got in zip(w, scales[:, 0]):
+            low, high = min(row.min(), 0.0), max(row.max(), 0.0)
+            width = (Fraction(float(np.float32(high - low))) if with_zeros
+                     else Fraction(float(max(high, -low))))
+            raw = np.float32(float(width * factor))  # (48 bits: exact in float64)
+            assert got == ot.round_to(np.array([raw]), scale_type)[0]
+            assert abs(Fraction(float(raw)) - width / steps) <= Fraction(2) ** -23 * width / steps
