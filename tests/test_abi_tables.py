@@ -182,3 +182,76 @@ def test_gradients_that_are_too_wide_are_refused_before_any_work(sp):
         10, d, 0, p, d, 4, 4, 2 * p, 1.0, 0, 0, 3 * p, d, 4 * p, 1 << 35, None)
     assert call(dim) == sp.SPMV_ERR_TOO_LARGE
     assert call(dim - 1) != sp.SPMV_ERR_TOO_LARGE
+
+
+# Arguments that are right but for their addresses, which are far apart and of no memory:
+# without a GPU they reach the CUDA call that looks them up, so that what a test below makes
+# wrong is what is refused. (With a GPU that call refuses the addresses.)
+A = 1 << 32
+GOOD = {
+    "spmv_q4_run": lambda sp, m: [C.byref(m), 2, 0, 4 * A, 64, 5 * A, 4, 0, 6 * A, 4, None],
+    "spmv_q4_quantize": lambda sp, m: [C.byref(m), 0, 4 * A, 64, 5 * A, 64, None],
+    "spmv_embed_q4": lambda sp, m: [C.byref(m), 4, 4, 4 * A, 1.0, 0, 5 * A, 64, None],
+    "spmv_embed": lambda sp, m: [10, 16, 0, 4 * A, 16, 4, 4, 5 * A, 1.0, 0, 6 * A, 16, None],
+    "spmv_embed_grad": lambda sp, m: [10, 16, 0, 4 * A, 16, 4, 4, 5 * A, 1.0, 0, 0, 6 * A, 16,
+                                      7 * A, 1 << 20, None],
+}
+MATRIX = dict(codes=A, scales=2 * A, zeros=3 * A, ld_zeros=2)
+
+
+def answer(sp, name, at=None, value=None, **matrix):
+    args = GOOD[name](sp, q4(sp, **{**MATRIX, **matrix}))
+    if at is not None:
+        args[at] = value
+    return getattr(sp._lib, name)(*args)
+
+
+def refused_for_this_alone(sp, name, *change, **matrix):
+    if not torch.cuda.is_available():
+        assert answer(sp, name) == sp.SPMV_ERR_CUDA
+    assert answer(sp, name, *change, **matrix) == sp.SPMV_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", ["spmv_q4_run", "spmv_q4_quantize", "spmv_embed_q4"])
+@pytest.mark.parametrize("bad", [{**b, "scales": 2 * A + 2} if "scales" in b and b["scales"]
+                                 else b for b in BAD_Q4 if b.get("zeros") != 4096]
+                         + [dict(ld_zeros=1)])
+def test_one_fault_of_a_matrix_is_enough(sp, name, bad):
+    refused_for_this_alone(sp, name, **bad)
+
+
+@pytest.mark.parametrize("name,at,value", [
+    ("spmv_q4_run", 1, -1), ("spmv_q4_run", 2, 3), ("spmv_q4_run", 3, None),
+    ("spmv_q4_run", 3, 4 * A + 2), ("spmv_q4_run", 3, 6 * A - 4), ("spmv_q4_run", 4, 63),
+    ("spmv_q4_run", 5, 6 * A + 4), ("spmv_q4_run", 5, 5 * A + 1), ("spmv_q4_run", 6, 3),
+    ("spmv_q4_run", 7, -1), ("spmv_q4_run", 8, None), ("spmv_q4_run", 8, 6 * A + 2),
+    ("spmv_q4_run", 8, A), ("spmv_q4_run", 8, 2 * A), ("spmv_q4_run", 8, 3 * A + 4),
+    ("spmv_q4_run", 9, 3),
+    ("spmv_q4_quantize", 1, 3), ("spmv_q4_quantize", 2, None), ("spmv_q4_quantize", 2, 4 * A + 1),
+    ("spmv_q4_quantize", 2, A), ("spmv_q4_quantize", 2, 2 * A + 4), ("spmv_q4_quantize", 3, 63),
+    ("spmv_q4_quantize", 4, 4 * A + 4), ("spmv_q4_quantize", 4, 3 * A + 4),
+    ("spmv_q4_quantize", 5, 63),
+    ("spmv_embed_q4", 1, -1), ("spmv_embed_q4", 2, 2), ("spmv_embed_q4", 3, 4 * A + 2),
+    ("spmv_embed_q4", 5, 3), ("spmv_embed_q4", 6, None), ("spmv_embed_q4", 6, 5 * A + 1),
+    ("spmv_embed_q4", 6, A), ("spmv_embed_q4", 6, 4 * A), ("spmv_embed_q4", 7, 63),
+    ("spmv_embed", 0, -1), ("spmv_embed", 1, -1), ("spmv_embed", 2, 3), ("spmv_embed", 3, None),
+    ("spmv_embed", 3, 4 * A + 2), ("spmv_embed", 4, 15), ("spmv_embed", 5, -1),
+    ("spmv_embed", 6, 2), ("spmv_embed", 7, None), ("spmv_embed", 7, 5 * A + 2),
+    ("spmv_embed", 9, -1), ("spmv_embed", 10, None), ("spmv_embed", 10, 4 * A + 4),
+    ("spmv_embed", 10, 5 * A), ("spmv_embed", 11, 15),
+    ("spmv_embed_grad", 0, -1), ("spmv_embed_grad", 1, -1), ("spmv_embed_grad", 2, 3),
+    ("spmv_embed_grad", 3, None), ("spmv_embed_grad", 3, 4 * A + 2),
+    ("spmv_embed_grad", 3, 6 * A + 4), ("spmv_embed_grad", 4, 15), ("spmv_embed_grad", 5, -1),
+    ("spmv_embed_grad", 6, 16), ("spmv_embed_grad", 7, None), ("spmv_embed_grad", 7, 6 * A),
+    ("spmv_embed_grad", 9, 2), ("spmv_embed_grad", 10, 3), ("spmv_embed_grad", 11, None),
+    ("spmv_embed_grad", 12, 15), ("spmv_embed_grad", 13, None),
+    ("spmv_embed_grad", 13, 7 * A + 8), ("spmv_embed_grad", 13, 4 * A),
+    ("spmv_embed_grad", 14, 16)])
+def test_one_fault_of_an_argument_is_enough(sp, name, at, value):
+    refused_for_this_alone(sp, name, at, value)
+
+
+def test_rows_without_tokens_are_no_more_than_the_table_has(sp):
+    refused_for_this_alone(sp, "spmv_embed_q4", 3, None, rows=3)
+    if not torch.cuda.is_available():
+        assert answer(sp, "spmv_embed_q4", 3, None) == sp.SPMV_ERR_CUDA
