@@ -132,6 +132,35 @@ def test_gradient(sp, kind, n, g_type, out_type, dim, vocab):
     check_grad(host(dt), g, tokens, vocab, -0.5, out_type, base)
 
 
+@pytest.mark.parametrize("terms", ["equal", "positive", "mixed"])
+@pytest.mark.parametrize("n,vocab,dim,g_type", [(4097, 1000, 256, "f32"), (19_000, 9, 256, "f32"),
+                                                (19_000, 40_000, 300, "bf16"),
+                                                (60_000, 2, 64, "f32"), (70_000, 5, 33, "f16"),
+                                                (3000, 7, 1000, "bf16")])
+def test_long_rows_of_terms_of_one_sign(sp, terms, n, vocab, dim, g_type):
+    """Most tokens are one, and the errors of its sum do not cancel. The chain of additions
+    behind a row of m terms, whatever the split: up to 32 in a chunk (twice that where a
+    row ends in the next one); a partial sum for each 4 terms at least, added in 4
+    groups at least, so m / 16 at most; 8 for joining the groups; the first chunk's sum,
+    the scale and the table's own value: (64 + m / 16 + 12) * 2^-24 of the magnitudes."""
+    rng = np.random.default_rng(n)
+    tokens = np.full(n, vocab // 2)
+    tokens[::50] = rng.integers(0, vocab, len(tokens[::50]))
+    g = {"equal": lambda: np.full((n, dim), 0.1), "positive": lambda: rng.random((n, dim)),
+         "mixed": lambda: rng.standard_normal((n, dim))}[terms]()
+    g = ot.round_to(g.astype(np.float32), g_type)
+    base = rng.random((vocab, dim)).astype(np.float32)
+    for add in (False, True):
+        dt = dev(base)
+        sp.spmv_embed_grad(dev(g, g_type), dev(tokens), dt, scale=0.3, accumulate=add)
+        want, mag, m = ot.embed_grad(g, tokens, vocab, float(np.float32(0.3)),
+                                     base if add else None)
+        bound = (np.minimum(m, 64) + m / 16 + 12)[:, None] * 2.0 ** -24 * mag
+        err = np.abs(host(dt).astype(np.float64) - want)
+        assert np.all(err <= bound + 2.0 ** -150), float((err / bound).max())
+        assert np.all(bound <= 3e-4 * mag)  # a term of ten thousand that is missing shows
+
+
 @pytest.mark.parametrize("n,vocab,kind", [(65536, 50000, "skewed"), (65537, 200, "uniform"),
                                           (70001, 300_000, "skewed"), (200_000, 3, "uniform"),
                                           (40_000, 131072, "one"), (16384, 2 ** 18 + 1, "ends")])
