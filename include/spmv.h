@@ -366,6 +366,8 @@ int spmv_run_csr_noalloc(int32_t numRows, int32_t numCols, int32_t nnz,
  * dimensions (ld...) count elements (codes: bytes) from one row to the next
  * and are at least the row's width; 64-bit offsets throughout. Sums and
  * scales are computed in fp32 and results rounded once to the output's type.
+ * Whether arrays overlap is judged by their ranges, each from its first element to
+ * its last (columns of one wide array, side by side, overlap).
  * Results are the same from call to call: no sum depends on the order in
  * which blocks run.
  * ------------------------------------------------------------------------- */

@@ -286,7 +286,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 # Memory of the current device for work on a stream (its handle), from torch's
 # allocator, which hands out again what is freed only behind what that stream was given
 # before; and the way back. By the calls below torch's public ones, where this torch has
-# them: a tensor instead cost 7 us more, of 12, and one more Python call each about 1.
+# them (a tensor instead cost 7 us more, of 12).
 def _public_take(nbytes, stream):
     return torch.cuda.caching_allocator_alloc(nbytes, stream=stream)
 

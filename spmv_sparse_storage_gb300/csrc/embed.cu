@@ -298,7 +298,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(
 constexpr int kSumThreads = 256;
 constexpr int kSumChunk = 32;       // positions of a chunk, at most
 constexpr int kSumChunkLeast = 4;
-constexpr int kSumWanted = 608;     // blocks: four for each SM
+constexpr int kSumWanted = 608;     // blocks: four for each of 152 SMs (a fixed number, so that
+                                    // the workspace is the same size wherever it is asked for)
 constexpr int kSumStaged = 1024;    // positions of a block, at most
 constexpr int kZeroRows = 64;       // rows of a zeroing block
 constexpr int kJoinChunks = 1024;   // chunks that a block of the second kernel looks at

@@ -11,9 +11,12 @@
 // bf16's least number (2^-133) even of a subnormal x, and no part is larger than
 // |x| or 2^-125; their sums are added with these weights at the end.
 //
-// What bounds it: with 1 to 8 columns the bytes of A, half a byte per entry and one
-// scale per group, read once for up to 16 columns, and close behind the
-// instructions that turn a nibble into a 16-bit operand (11 per 8 entries).
+// What bounds it: with 1 to 8 columns latency. The bytes of A, half a byte per entry
+// and one scale per group, are read once for up to 16 columns; the instructions that
+// turn a nibble into a 16-bit operand (11 per 8 entries) come close behind; but with
+// 128 registers, which hold the scales of two steps, only 16 warps run on an SM, DRAM
+// is busy for 0.48 to 0.59 of the time and the SM for 0.43 to 0.52 (43 of the 72 forms
+// spill, 164 bytes at most, in those with groups of 32 and zero points).
 // 131072 x 4096 with an fp32 vector and fp32 scales takes 57.7 us, 4.95 TB/s or
 // 0.73 of a copy (46.9 us without the scales' loads, the staging of x and the
 // joins); 8192 x 28672 with a bf16 vector 29.4 us, 4.1 TB/s (24.6 without the
